@@ -55,7 +55,9 @@ extern "C" {
 
 /* 3: adds fkv_fp8_cache_t and the three *_fp8 entry points;
  * 4: adds fkv_select_heuristic; 5: adds fkv_step_fp8;
- * 6: adds fkv_diag_attend_timeout, fkv_diag_mma_rate, fkv_diag_ex2_rate. */
+ * 6: adds fkv_diag_attend_timeout, fkv_diag_mma_rate, fkv_diag_ex2_rate, and
+ *    (no earlier struct or entry point changed) the paged cache: fkv_paged_t
+ *    and the fkv_paged_* entry points, fkv_qk_norm_rope. */
 #define FKV_ABI_VERSION 6
 
 typedef enum fkv_status {
@@ -460,6 +462,144 @@ int32_t fkv_attend_compressed_fp8(const fkv_params_t* p, const fkv_fp8_cache_t* 
  * launch. */
 int32_t fkv_step_fp8(const fkv_params_t* p, const fkv_step_io_t* io, const fkv_fp8_cache_t* c,
                      void* ws, void* stream);
+
+/* ---- Paged cache -------------------------------------------------------------
+ * The chunk step above takes keys that are already normed and rotated, in a
+ * dense per-head cache.  The entry points below make those keys
+ * (fkv_qk_norm_rope), and keep and read the cache of a serving loop whose
+ * sequences have different lengths (fkv_paged_append, fkv_paged_decode,
+ * fkv_paged_attend).
+ *
+ * Rows: queries, keys, values and outputs are [tokens][heads][D] with element
+ * strides (fkv_rows_t; D contiguous).  Pages: the cache is k_cache / v_cache
+ * [num_pages][Hkv][page_size][D] with element strides of page, head and row
+ * (the same for both; D contiguous), so the layouts "heads outside rows" and
+ * "rows outside heads", and a dense cache read as one run of pages, are all
+ * valid.  Position p of sequence b lives in page page_table[b][p / page_size],
+ * row p % page_size.  Two sequences may share pages (a common prefix) as long
+ * as no call appends to a shared page.
+ *
+ * Batches are ragged: cu_q[0..B] are the token offsets of the B sequences
+ * (ascending, cu_q[0] = 0), kv_len[b] the cached length of sequence b WITH the
+ * tokens of this call, so that token i of the q_len = cu_q[b+1] - cu_q[b] new
+ * ones has position kv_len[b] - q_len + i.  cu_q NULL: one token per sequence.
+ * Rows of tokens at or behind cu_q[B] (a padded batch) are neither read nor
+ * written.  num_tokens bounds the row arrays.
+ *
+ * Every base pointer is 16-byte aligned and every stride a multiple of 16
+ * bytes (strides of dimensions of size 1 are ignored).  Output rows must not
+ * overlap one another or any input, except where an entry point says so.
+ * bf16 or fp32 throughout (dtype); D is 64 or 128; page_size is a power of
+ * two, 8 .. 1024; at most 8192 sequences, max_pages * page_size <= 2^30, and
+ * fewer than 2^31 tokens.
+ *
+ * Device-side errors, recorded as FKV_ERR_DEVICE_ARG in the workspace status
+ * word with the sequence as detail (nothing is read or written out of range):
+ * cu_q not ascending or above num_tokens (the sequence counts as empty),
+ * kv_len outside 0 .. max_pages * page_size (clamped), a page id outside
+ * 0 .. num_pages - 1 where a row is needed (an append drops the row; a read
+ * sees rows of zeros), an appended token with a negative position (its key and
+ * value are dropped).  A query at a negative position is no error: under
+ * FKV_PAGED_CAUSAL it sees the prefix alone. */
+#define FKV_PAGED_CAUSAL 1 /* query at position p sees keys j <= p; without it
+                              every key of its sequence */
+typedef struct fkv_paged {
+  int32_t dtype;        /* fkv_dtype_t of q, k, v, caches and outputs            */
+  int32_t flags;        /* FKV_PAGED_* bits                                      */
+  int32_t head_dim;     /* D: 64 or 128                                          */
+  int32_t num_q_heads;  /* Hq: a multiple of Hkv; query head h reads the keys of
+                           head h / (Hq / Hkv)                                   */
+  int32_t num_kv_heads; /* Hkv >= 1                                              */
+  int32_t page_size;    /* rows per page: a power of two, 8 .. 1024              */
+  int32_t num_pages;    /* pages of the cache, >= 0                              */
+  int32_t num_seqs;     /* B >= 0                                                */
+  int32_t max_pages;    /* entries per sequence of page_table, >= 0              */
+  int32_t window;       /* W >= 0; W > 0: a query at position p sees keys
+                           j > p - W only (and the prefix)                       */
+  float scale;          /* scale of q.k, finite and > 0                          */
+  float softcap;        /* c >= 0, finite; c > 0: scores c * tanh(scale q.k / c) */
+  int64_t page_stride, head_stride, row_stride; /* of the caches, in elements    */
+  int64_t table_stride; /* elements between sequences of page_table              */
+  void* k_cache;
+  void* v_cache;
+  const int32_t* page_table;
+  const int32_t* kv_len;     /* [B]                                              */
+  const int32_t* cu_q;       /* [B + 1], or NULL: one token per sequence         */
+  const int32_t* prefix_len; /* [B] or NULL (no prefix): keys j < prefix_len[b]
+                                are seen by every query of sequence b, whatever
+                                order and window say                             */
+  const float* alibi_slopes; /* [Hq] or NULL: adds slope[h] * (j - p) to the
+                                score of key j and a query at position p         */
+} fkv_paged_t;
+
+typedef struct fkv_rows {
+  void* ptr;
+  int64_t token_stride, head_stride; /* in elements                              */
+} fkv_rows_t;
+
+/* Per-head RMS norm and rotation of rows.  With norm != 0 a row x becomes
+ * x / sqrt(mean(x^2) + eps) * weight (weight NULL: ones).  Then the pairs
+ * i < n = axis_pairs[0] + .. + axis_pairs[n_axes - 1] of dims (2i, 2i + 1)
+ * (FKV_ROPE_ADJACENT, the pairs of fkv_compact_gather_rope) or (i, i + n)
+ * (FKV_ROPE_HALF; n a multiple of 8) are turned by the angle
+ * omega[i] * positions[axis of i][token], the first axis_pairs[0] pairs by
+ * axis 0, the next by axis 1, and so on (video: frame, row, column); the other
+ * dims keep their values.  Angles are formed and reduced in 64 bits, the rest
+ * is fp32, and each value is rounded once. */
+#define FKV_ROPE_ADJACENT 0
+#define FKV_ROPE_HALF 1
+typedef struct fkv_rope {
+  int32_t style;         /* FKV_ROPE_*                                           */
+  int32_t norm;          /* 0: rotate only                                       */
+  int32_t n_axes;        /* 1 .. 3                                               */
+  int32_t axis_pairs[3]; /* >= 0, 2 * their sum <= D                             */
+  float eps;             /* >= 0, finite                                         */
+  const float* q_weight; /* [D] or NULL                                          */
+  const float* k_weight; /* [D] or NULL                                          */
+  const float* omega;    /* [n]; may be NULL when n == 0                         */
+  const int32_t* positions; /* [n_axes][axis_stride]; fkv_paged_append with one
+                               axis: NULL = the cache position                   */
+  int64_t axis_stride;   /* >= num_tokens (n_axes > 1)                           */
+} fkv_rope_t;
+
+/* Norm and rotation of num_tokens rows of queries (Hq heads) and keys (Hkv
+ * heads) in one launch; either head count may be 0 (its rows unused).  q_out /
+ * k_out may be q / k themselves (same pointer and strides), or any layout with
+ * the strides of fkv_rows_t: head-major outputs are what fkv_step takes. */
+int32_t fkv_qk_norm_rope(const fkv_rope_t* r, int32_t dtype, int32_t head_dim, int32_t num_tokens,
+                         int32_t num_q_heads, int32_t num_kv_heads, const fkv_rows_t* q,
+                         const fkv_rows_t* k, const fkv_rows_t* q_out, const fkv_rows_t* k_out,
+                         void* stream);
+
+/* Bytes of workspace of the paged entry points (zeroed once with
+ * fkv_workspace_init, 256-byte aligned; the status block, then the partial
+ * results of work split over the keys).  The same for every fkv_paged_t. */
+int32_t fkv_paged_workspace_size(size_t* bytes);
+
+/* Appends num_tokens new rows of k and v to the cache at their positions, with
+ * the norm and rotation of r on the keys (r NULL: keys as they are).  With q,
+ * the queries get the norm and rotation too, in the same launch, and go to
+ * q_out (q may be q_out; q NULL: keys and values only). */
+int32_t fkv_paged_append(const fkv_paged_t* c, const fkv_rope_t* r, int32_t num_tokens,
+                         const fkv_rows_t* q, const fkv_rows_t* k, const fkv_rows_t* v,
+                         const fkv_rows_t* q_out, void* ws, void* stream);
+
+/* Attention of one query token per sequence (q, out: [B][Hq][D]) over the
+ * cache; the query of sequence b has position kv_len[b] - 1 (cu_q is not
+ * used).  out[b][h] = sum_j softmax_j(score_j) v_j over the keys that the
+ * masks of c leave, fp32 accumulation, rounded once; lse[b][h] (float
+ * [B][Hq], may be NULL) = log sum_j exp(score_j).  No key left (kv_len 0):
+ * zeros, and lse = -inf.  Masked keys and values may hold anything, NaN
+ * included. */
+int32_t fkv_paged_decode(const fkv_paged_t* c, const fkv_rows_t* q, const fkv_rows_t* out,
+                         float* lse, void* ws, void* stream);
+
+/* The same for a ragged batch of num_tokens query tokens (cu_q; q, out:
+ * [num_tokens][Hq][D], lse [num_tokens][Hq]).  Keys and values that no query
+ * of the sequence sees may hold anything; a value row that some query of the
+ * sequence sees must be finite. */
+int32_t fkv_paged_attend(const fkv_paged_t* c, int32_t num_tokens, const fkv_rows_t* q,
+                         const fkv_rows_t* out, float* lse, void* ws, void* stream);
 
 #ifdef __cplusplus
 }

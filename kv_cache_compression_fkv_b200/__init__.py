@@ -31,6 +31,8 @@ __all__ = [
     "select_topk", "compact_gather", "attend_compressed", "step", "read_status", "library",
     "step_launches", "make_step_io", "score_segments_noalloc", "cache_advance",
     "compact_gather_rope", "marshal",
+    "Rope", "make_rope", "qk_norm_rope", "PagedCache", "paged_append", "paged_decode",
+    "paged_attend",
 ]
 
 
@@ -471,3 +473,7 @@ def read_status(ws: torch.Tensor, stream=None):
     _check(_lib.load().fkv_read_status(ws.data_ptr(), _stream(stream), ctypes.byref(a), ctypes.byref(b)),
            "fkv_read_status")
     return a.value, b.value
+
+
+from .paged import (PagedCache, Rope, make_rope, paged_append, paged_attend,  # noqa: E402
+                    paged_decode, qk_norm_rope)

@@ -22,6 +22,9 @@ FKV_GRAN_FRAME = 0
 FKV_GRAN_TOKEN = 1
 FKV_FLAG_SCORE_WITH_CHUNK = 1
 FKV_FLAG_STATIC_TOKEN_MASK = 2
+FKV_PAGED_CAUSAL = 1
+FKV_ROPE_ADJACENT = 0
+FKV_ROPE_HALF = 1
 FKV_POLICY_UNIFORM = 0
 FKV_POLICY_RANDOM = 1
 
@@ -64,6 +67,35 @@ class Fp8Cache(ctypes.Structure):
     _fields_ = [(n, c_vp) for n in FP8_CACHE_FIELDS]
 
 
+class Paged(ctypes.Structure):
+    """fkv_paged_t."""
+
+    _fields_ = [
+        ("dtype", c_i32), ("flags", c_i32), ("head_dim", c_i32), ("num_q_heads", c_i32),
+        ("num_kv_heads", c_i32), ("page_size", c_i32), ("num_pages", c_i32), ("num_seqs", c_i32),
+        ("max_pages", c_i32), ("window", c_i32), ("scale", c_f32), ("softcap", c_f32),
+        ("page_stride", c_i64), ("head_stride", c_i64), ("row_stride", c_i64),
+        ("table_stride", c_i64), ("k_cache", c_vp), ("v_cache", c_vp), ("page_table", c_vp),
+        ("kv_len", c_vp), ("cu_q", c_vp), ("prefix_len", c_vp), ("alibi_slopes", c_vp),
+    ]
+
+
+class Rows(ctypes.Structure):
+    """fkv_rows_t."""
+
+    _fields_ = [("ptr", c_vp), ("token_stride", c_i64), ("head_stride", c_i64)]
+
+
+class Rope(ctypes.Structure):
+    """fkv_rope_t."""
+
+    _fields_ = [
+        ("style", c_i32), ("norm", c_i32), ("n_axes", c_i32), ("axis_pairs", c_i32 * 3),
+        ("eps", c_f32), ("q_weight", c_vp), ("k_weight", c_vp), ("omega", c_vp),
+        ("positions", c_vp), ("axis_stride", c_i64),
+    ]
+
+
 # name -> (restype, argtypes), exactly the declarations of include/fkv.h
 SIGNATURES = {
     "fkv_status_string": (ctypes.c_char_p, [c_i32]),
@@ -99,6 +131,17 @@ SIGNATURES = {
                                           c_vp, c_vp, c_vp]),
     "fkv_step_fp8": (c_i32, [ctypes.POINTER(Params), ctypes.POINTER(StepIO), ctypes.POINTER(Fp8Cache),
                              c_vp, c_vp]),
+    "fkv_qk_norm_rope": (c_i32, [ctypes.POINTER(Rope), c_i32, c_i32, c_i32, c_i32, c_i32,
+                                 ctypes.POINTER(Rows), ctypes.POINTER(Rows), ctypes.POINTER(Rows),
+                                 ctypes.POINTER(Rows), c_vp]),
+    "fkv_paged_workspace_size": (c_i32, [ctypes.POINTER(c_sz)]),
+    "fkv_paged_append": (c_i32, [ctypes.POINTER(Paged), ctypes.POINTER(Rope), c_i32,
+                                 ctypes.POINTER(Rows), ctypes.POINTER(Rows), ctypes.POINTER(Rows),
+                                 ctypes.POINTER(Rows), c_vp, c_vp]),
+    "fkv_paged_decode": (c_i32, [ctypes.POINTER(Paged), ctypes.POINTER(Rows), ctypes.POINTER(Rows),
+                                 c_vp, c_vp, c_vp]),
+    "fkv_paged_attend": (c_i32, [ctypes.POINTER(Paged), c_i32, ctypes.POINTER(Rows),
+                                 ctypes.POINTER(Rows), c_vp, c_vp, c_vp]),
 }
 
 _lib = None

@@ -1,0 +1,319 @@
+// Shared pieces of the paged-cache attention kernels: the resolved arguments,
+// what a tile of query rows can see, the division of the work over CTAs, and
+// the partial results that a split leaves behind.
+//
+// Work.  A unit is one tile of query rows of one sequence against one KV head:
+// the G = Hq / Hkv query heads that share the KV head are packed with `tq`
+// tokens into the tile's R rows (row r = token r / G, head r % G; with G > R one
+// token and a slice of R heads).  A unit costs as many steps as the key blocks
+// of TK keys that any of its rows can see; blocks that no row sees are never
+// loaded.  The units of the batch, ordered (sequence, query tile, head), laid
+// end to end make one line of steps that is cut into equal parts, one per CTA,
+// whatever the lengths are.  The cut is made on the GPU from cu_q, kv_len and
+// prefix_len, so a captured call stays valid when the lengths change.
+//
+// Join.  A unit cut by a part boundary is finished by paged_join_kernel from
+// the partial softmaxes (maximum, sum, unnormalised output, all fp32) of the
+// CTAs that share it.  A CTA leaves at most two: of its first unit (slot 0)
+// and of its last (slot 1).  They are merged in CTA order, so results do not
+// depend on timing.
+#pragma once
+
+#include "fkv_internal.cuh"
+#include "paged_plan.h"
+
+namespace fkv {
+
+constexpr int kMaxPagedSeqs = 8192;  // prefix sums of the division fit in shared memory
+constexpr int kMaxPagedCtas = 296;   // partial slots are sized for two CTAs per SM
+
+struct PagedArgs : TileRule {
+  const int32_t* page_table;
+  const int32_t* kv_len;
+  const int32_t* cu_q;
+  const int32_t* prefix_len;
+  const float* slopes;
+  int64_t table_stride;
+  int B, Hq;
+  int page_shift, num_pages, max_pages, num_tokens;
+  int min_steps;  // smallest part worth a CTA
+  float scale, cap;
+  // rows
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_ts, q_hs, o_ts, o_hs;
+  // caches (element strides)
+  const void* k_cache;
+  const void* v_cache;
+  int64_t page_stride, head_stride, row_stride;
+  // workspace
+  int32_t* status;
+  struct PlanRec* rec;  // [kMaxPagedCtas]
+  float2* part_ml;      // [slot][R] (max in base 2, sum)
+  float* part_o;        // [slot][R][D]
+};
+
+// Where a CTA's part of the line begins.
+struct PlanRec {
+  int b, qt, hm, j;  // sequence, query tile, head unit, step inside the unit
+  int n;             // steps of that unit
+  int per;           // steps per part
+  int count;         // steps of this part (0: none)
+  int pad;
+};
+
+__device__ __forceinline__ Seq load_seq(const PagedArgs& a, int b) {
+  Seq s;
+  if (a.cu_q) {
+    s.q0 = a.cu_q[b];
+    const int e = a.cu_q[b + 1];
+    s.q_len = e - s.q0;
+    if (s.q0 < 0 || e < s.q0 || e > a.num_tokens) {
+      report(a.status, FKV_ERR_DEVICE_ARG, b);
+      s.q0 = 0;
+      s.q_len = 0;
+    }
+  } else {
+    s.q0 = b;
+    s.q_len = 1;
+  }
+  const int cap = a.max_pages << a.page_shift;
+  const int kv = a.kv_len[b];
+  s.kv = kv < 0 ? 0 : (kv > cap ? cap : kv);
+  if (s.kv != kv) report(a.status, FKV_ERR_DEVICE_ARG, b);
+  const int pre = a.prefix_len ? a.prefix_len[b] : 0;
+  s.pre = pre < 0 ? 0 : (pre > s.kv ? s.kv : pre);
+  return s;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Steps of one sequence (one KV-head unit), computed by the whole warp.
+__device__ __forceinline__ int64_t seq_steps_warp(const PagedArgs& a, int b, int lane) {
+  const Seq s = load_seq(a, b);
+  const int nq = query_tiles(a, s);
+  int64_t w = 0;
+  for (int qt = lane; qt < nq; qt += 32) w += tile_span(a, s, qt).n;
+  return warp_sum(w);
+}
+
+// The division: every thread of the CTA calls it; `cum` is shared scratch of
+// B + 1 int64 (free again after the next __syncthreads), `rec` the shared
+// result.  Ends with a __syncthreads.
+template <int kThreads>
+__device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* cum, PlanRec* rec) {
+  __shared__ int64_t warp_tot[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hm_n = a.Hkv * a.mt;
+  int64_t carry = 0;
+  if (tid == 0) cum[0] = 0;
+  for (int base = 0; base < a.B; base += kThreads) {
+    const int b = base + tid;
+    int64_t w = 0;
+    bool wide = false;
+    if (b < a.B) {
+      const Seq s = load_seq(a, b);
+      const int nq = query_tiles(a, s);
+      wide = nq > 2;
+      if (!wide)
+        for (int qt = 0; qt < nq; ++qt) w += tile_span(a, s, qt).n;
+    }
+    // sequences of many query tiles are counted by the warp together
+    unsigned todo = __ballot_sync(0xffffffffu, wide);
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int64_t t = seq_steps_warp(a, base + (warp << 5) + src, lane);
+      if (lane == src) w = t;
+    }
+    w *= hm_n;
+    int64_t inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_tot[warp] = inc;
+    __syncthreads();
+    int64_t before = carry, all = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += warp_tot[i];
+      all += warp_tot[i];
+    }
+    if (b < a.B) cum[b + 1] = before + inc;
+    carry += all;
+    __syncthreads();
+  }
+  if (warp == 0) {
+    const int64_t total = carry;
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < a.min_steps) per = a.min_steps;
+    const int64_t start = per * blockIdx.x;
+    int64_t count = total - start < per ? total - start : per;
+    if (count < 0) count = 0;
+    PlanRec r = {};
+    r.per = int(per);
+    r.count = int(count);
+    if (count > 0) {
+      int lo = 0, hi = a.B - 1;  // the sequence with cum[b] <= start < cum[b + 1]
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid + 1] > start) hi = mid;
+        else lo = mid + 1;
+      }
+      r.b = lo;
+      const Seq s = load_seq(a, lo);
+      const int nq = query_tiles(a, s);
+      int64_t rest = start - cum[lo];
+      for (int q0 = 0; q0 < nq; q0 += 32) {
+        const int qt = q0 + lane;
+        const int n = qt < nq ? tile_span(a, s, qt).n : 0;
+        int64_t inc = int64_t(n) * hm_n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, inc > rest);
+        if (past) {
+          const int src = __ffs(past) - 1;
+          const int64_t in_tile = rest - (inc - int64_t(n) * hm_n);  // lane src: steps into its tile
+          const int64_t in = __shfl_sync(0xffffffffu, in_tile, src);
+          r.n = __shfl_sync(0xffffffffu, n, src);
+          r.qt = q0 + src;
+          r.hm = int(in / r.n);
+          r.j = int(in - int64_t(r.hm) * r.n);
+          break;
+        }
+        rest -= __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    if (lane == 0) {
+      *rec = r;
+      a.rec[blockIdx.x] = r;
+    }
+  }
+  __syncthreads();
+}
+
+// Walks the units of a part.  All roles of a CTA walk alike.
+struct Walk {
+  Seq s;
+  Span t;
+  int b, qt, hm, j, left, index;
+
+  __device__ __forceinline__ void begin(const PagedArgs& a, const PlanRec& r) {
+    b = r.b;
+    qt = r.qt;
+    hm = r.hm;
+    j = r.j;
+    left = r.count;
+    index = 0;
+    if (left > 0) {
+      s = load_seq(a, b);
+      t = tile_span(a, s, qt);
+    }
+  }
+  __device__ __forceinline__ bool done() const { return left <= 0; }
+  // Steps of the current unit that belong to this part.
+  __device__ __forceinline__ int steps() const { return t.n - j < left ? t.n - j : left; }
+  __device__ __forceinline__ bool whole() const { return j == 0 && left >= t.n; }
+  __device__ __forceinline__ int slot() const {
+    return 2 * int(blockIdx.x) + (index == 0 ? 0 : 1);
+  }
+  __device__ __forceinline__ void next(const PagedArgs& a) {
+    left -= steps();
+    ++index;
+    j = 0;
+    if (left <= 0) return;
+    if (++hm < a.Hkv * a.mt) return;
+    hm = 0;
+    if (++qt >= query_tiles(a, s)) {
+      qt = 0;
+      do {
+        s = load_seq(a, ++b);
+      } while (s.q_len == 0);
+    }
+    t = tile_span(a, s, qt);
+  }
+};
+
+// Page id of a sequence's p-th page; -1 (reported) when out of range.
+__device__ __forceinline__ int page_id(const PagedArgs& a, int b, int p) {
+  const int id = a.page_table[int64_t(b) * a.table_stride + p];
+  if (id >= 0 && id < a.num_pages) return id;
+  report(a.status, FKV_ERR_DEVICE_ARG, b);
+  return -1;
+}
+
+// c * tanh(x) without cancellation loss beyond one rounding of the absolute
+// value: tanh(x) = 1 - 2 / (e^2x + 1); exact limits at +-inf.
+__device__ __forceinline__ float tanh_fast(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 2.885390081777927f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+  return fmaf(-2.f, r, 1.f);
+}
+
+struct PagedWs {
+  size_t rec, ml, o, total;
+};
+inline PagedWs paged_ws_layout() {
+  // slots x rows is largest for the 128-row tiles with one CTA per SM
+  // (148 * 2 slots * 128 rows); 16-row tiles have 296 * 2 * 16.
+  PagedWs w;
+  const size_t rows = size_t(kMaxPagedCtas) * 128;
+  w.rec = 256;
+  w.ml = w.rec + sizeof(PlanRec) * kMaxPagedCtas;
+  w.ml = (w.ml + 255) & ~size_t(255);
+  w.o = w.ml + rows * sizeof(float2);
+  w.total = w.o + rows * 128 * sizeof(float);
+  return w;
+}
+
+// grid of a kernel with `per_sm` resident CTAs and R rows: every slot fits.
+inline int paged_grid(int per_sm) {
+  const int n = num_sms() * per_sm, most = per_sm * (kMaxPagedCtas / 2);
+  return n < most ? n : most;
+}
+
+// Arguments of the norm / rotation / append kernel (paged_rows.cu).
+struct RowsArgs {
+  int tokens, nq, nk, nv;  // heads per token (nv: value rows, append only)
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_out;             // rows of keys; unused by an append
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+  // norm and rotation
+  int norm, half, pairs, axis1, axis2;  // first pair of axis 1 and of axis 2
+  float eps;
+  const float* q_weight;
+  const float* k_weight;
+  const float* omega;
+  const int32_t* positions;  // NULL: the cache position
+  int64_t axis_stride;
+  // append
+  int append, B, page_shift, num_pages, max_pages;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t table_stride, page_stride, head_stride, row_stride;
+  void* k_cache;
+  void* v_cache;
+  int32_t* status;
+};
+
+cudaError_t launch_rows(const RowsArgs& a, bool bf16, int D, cudaStream_t s);
+cudaError_t launch_paged_join(const PagedArgs& a, int D, bool bf16, int grid, cudaStream_t s);
+cudaError_t launch_paged_simt(PagedArgs a, int D, cudaStream_t s);
+cudaError_t launch_paged_simt_bf16(PagedArgs a, int D, cudaStream_t s);
+
+}  // namespace fkv

@@ -16,7 +16,7 @@ int32_t launch_status(cudaError_t e) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-const int64_t kMaxStride = int64_t(1) << 40;
+const int64_t kMaxStride = int64_t(1) << 38;  // elements; tensor maps end at 2^40 bytes
 
 // Row strides as the kernels use them: 0 where the dimension has one entry.
 struct Strides {
@@ -189,6 +189,9 @@ int32_t attention(const fkv_paged_t* c, int64_t tokens, bool single, const fkv_r
   a.o_hs = so.hs;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c->dtype == FKV_DTYPE_FP32) return launch_status(launch_paged_simt(a, c->head_dim, s));
+  // tensor maps have no zero strides
+  if ((a.Hq > 1 && a.q_hs == 0) || (tokens > 1 && a.q_ts == 0)) return FKV_ERR_SHAPE;
+  if (single) return launch_status(launch_paged_decode(a, c->head_dim, s));
   return launch_status(launch_paged_simt_bf16(a, c->head_dim, s));
 }
 

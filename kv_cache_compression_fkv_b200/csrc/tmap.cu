@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "fkv_internal.cuh"
+#include "paged_common.cuh"
 #include "sm100_common.cuh"
 
 namespace fkv {
@@ -57,6 +58,38 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t sl
                   box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// bf16 map of up to four dimensions, rows of 64 dims in the 128-byte swizzle.
+static bool encode_bf16(CUtensorMap* map, const void* base, uint32_t rank, const cuuint64_t* dims,
+                        const cuuint64_t* strides, const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
+                  strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool paged_tmaps(const PagedArgs& a, int D, int keys, int q_heads, int q_tokens, CUtensorMap* q,
+                 CUtensorMap* k, CUtensorMap* v) {
+  const cuuint64_t one = cuuint64_t(D) * 2;  // stride of a dimension of one entry
+  const cuuint64_t q_dims[3] = {cuuint64_t(D), cuuint64_t(a.Hq), cuuint64_t(a.num_tokens)};
+  const cuuint64_t q_strides[2] = {a.Hq > 1 ? cuuint64_t(a.q_hs) * 2 : one,
+                                   a.num_tokens > 1 ? cuuint64_t(a.q_ts) * 2 : one};
+  const cuuint32_t q_box[3] = {64, cuuint32_t(q_heads), cuuint32_t(q_tokens)};
+  if (!encode_bf16(q, a.q, 3, q_dims, q_strides, q_box)) return false;
+  // A cache without pages gets a map of one page that no copy reads (every page
+  // id is then out of range, and reads as the zeros outside the map).
+  const bool none = a.num_pages == 0;
+  const int rows = 1 << a.page_shift;
+  const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(rows), cuuint64_t(a.Hkv),
+                              cuuint64_t(none ? 1 : a.num_pages)};
+  const cuuint64_t strides[3] = {cuuint64_t(a.row_stride) * 2, cuuint64_t(a.head_stride) * 2,
+                                 cuuint64_t(a.page_stride) * 2};
+  const cuuint32_t box[4] = {64, cuuint32_t(rows < keys ? rows : keys), 1, 1};
+  return encode_bf16(k, none ? a.q : a.k_cache, 4, dims, strides, box) &&
+         encode_bf16(v, none ? a.q : a.v_cache, 4, dims, strides, box);
 }
 
 int num_sms() {

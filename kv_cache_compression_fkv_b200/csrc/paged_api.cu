@@ -192,7 +192,7 @@ int32_t attention(const fkv_paged_t* c, int64_t tokens, bool single, const fkv_r
   // tensor maps have no zero strides
   if ((a.Hq > 1 && a.q_hs == 0) || (tokens > 1 && a.q_ts == 0)) return FKV_ERR_SHAPE;
   if (single) return launch_status(launch_paged_decode(a, c->head_dim, s));
-  return launch_status(launch_paged_simt_bf16(a, c->head_dim, s));
+  return launch_status(launch_paged_attend(a, c->head_dim, s));
 }
 
 }  // namespace

@@ -104,12 +104,13 @@ __device__ __forceinline__ int64_t seq_steps_warp(const PagedArgs& a, int b, int
   return warp_sum(w);
 }
 
-// The division: every thread of the CTA calls it; `cum` is shared scratch of
-// B + 1 int64 (free again after the next __syncthreads), `rec` the shared
-// result.  Ends with a __syncthreads.
+// The division: every thread of the CTA calls it; `scratch` is shared memory
+// (free again afterwards), `rec` the shared result.  Ends with a __syncthreads.
+constexpr size_t kPlanScratch = sizeof(int64_t) * (32 + kMaxPagedSeqs + 1);
 template <int kThreads>
-__device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* cum, PlanRec* rec) {
-  __shared__ int64_t warp_tot[kThreads / 32];
+__device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, PlanRec* rec) {
+  int64_t* warp_tot = scratch;     // [kThreads / 32]
+  int64_t* cum = scratch + 32;     // [B + 1] steps of the sequences before b
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hm_n = a.Hkv * a.mt;
   int64_t carry = 0;
@@ -319,8 +320,8 @@ cudaError_t launch_rows(const RowsArgs& a, bool bf16, int D, cudaStream_t s);
 bool paged_tmaps(const PagedArgs& a, int D, int keys, int q_heads, int q_tokens, CUtensorMap* q,
                  CUtensorMap* k, CUtensorMap* v);
 cudaError_t launch_paged_decode(const PagedArgs& a, int D, cudaStream_t s);
+cudaError_t launch_paged_attend(const PagedArgs& a, int D, cudaStream_t s);
 cudaError_t launch_paged_join(const PagedArgs& a, int D, bool bf16, int grid, cudaStream_t s);
 cudaError_t launch_paged_simt(PagedArgs a, int D, cudaStream_t s);
-cudaError_t launch_paged_simt_bf16(PagedArgs a, int D, cudaStream_t s);
 
 }  // namespace fkv

@@ -47,14 +47,6 @@ struct DecBars {
   int abort;
 };
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0,
-                                            int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -416,8 +408,7 @@ static cudaError_t launch_decode(PagedArgs a, cudaStream_t s) {
   CUtensorMap tq, tk, tv;
   if (!paged_tmaps(a, D, kDecKeys, kDecRows, 1, &tq, &tk, &tv)) return cudaErrorNotSupported;
   const size_t smem = 1024 + C::kOffBar + sizeof(DecBars);
-  static_assert(C::kStages * C::kStage >= (kMaxPagedSeqs + 1) * sizeof(int64_t),
-                "the division's prefix sums fit in the ring");
+  static_assert(C::kStages * C::kStage >= kPlanScratch, "the division's prefix sums fit in the ring");
   static_assert(2 * (1024 + C::kOffBar + sizeof(DecBars) + 1024 + 256) <= 233472,
                 "two CTAs per SM");
   auto* k = paged_decode_kernel<D>;

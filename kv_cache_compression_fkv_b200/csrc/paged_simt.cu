@@ -171,7 +171,7 @@ static cudaError_t launch_simt(PagedArgs a, cudaStream_t s) {
   a.mt = (a.G + R - 1) / R;
   a.tq = a.cu_q ? (a.mt == 1 ? R / a.G : 1) : 1;
   a.min_steps = 4;
-  const size_t plan = sizeof(int64_t) * (size_t(a.B) + 1);
+  const size_t plan = kPlanScratch;
   size_t smem = sizeof(float) * (R * D + kSimtKeys * (D + 4) + kSimtKeys * D);
   if (smem < plan) smem = plan;
   auto* k = paged_simt_kernel<T, D, R>;
@@ -185,9 +185,6 @@ static cudaError_t launch_simt(PagedArgs a, cudaStream_t s) {
 
 cudaError_t launch_paged_simt(PagedArgs a, int D, cudaStream_t s) {
   return D == 128 ? launch_simt<float, 128, 16>(a, s) : launch_simt<float, 64, 16>(a, s);
-}
-cudaError_t launch_paged_simt_bf16(PagedArgs a, int D, cudaStream_t s) {
-  return D == 128 ? launch_simt<__nv_bfloat16, 128, 16>(a, s) : launch_simt<__nv_bfloat16, 64, 16>(a, s);
 }
 
 }  // namespace fkv

@@ -590,14 +590,16 @@ int32_t fkv_paged_append(const fkv_paged_t* c, const fkv_rope_t* r, int32_t num_
  * masks of c leave, fp32 accumulation, rounded once; lse[b][h] (float
  * [B][Hq], may be NULL) = log sum_j exp(score_j).  No key left (kv_len 0):
  * zeros, and lse = -inf.  Masked keys and values may hold anything, NaN
- * included. */
+ * included.  Results are the same from call to call for the same batch; where
+ * the keys of a sequence are split, and so the last bit of its result, goes by
+ * all lengths of the batch. */
 int32_t fkv_paged_decode(const fkv_paged_t* c, const fkv_rows_t* q, const fkv_rows_t* out,
                          float* lse, void* ws, void* stream);
 
 /* The same for a ragged batch of num_tokens query tokens (cu_q; q, out:
  * [num_tokens][Hq][D], lse [num_tokens][Hq]).  Keys and values that no query
- * of the sequence sees may hold anything; a value row that some query of the
- * sequence sees must be finite. */
+ * of the sequence sees may hold anything; keys and values that some query of
+ * the sequence sees must be finite. */
 int32_t fkv_paged_attend(const fkv_paged_t* c, int32_t num_tokens, const fkv_rows_t* q,
                          const fkv_rows_t* out, float* lse, void* ws, void* stream);
 

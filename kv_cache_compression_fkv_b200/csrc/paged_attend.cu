@@ -39,18 +39,29 @@ constexpr int kPaK = 8, kPaV = 10, kPaMma = 9;  // warps: K and Q, V, MMA issuer
 constexpr float kPaRescale = 8.0f;              // P stays <= 2^8 between rescales
 constexpr int kPaPolyEvery = 8;                 // one exponential pair in 8 on the FMA pipe
 
+#ifndef FKV_PA_Q
+#define FKV_PA_Q 2
+#endif
+#ifndef FKV_PA_K
+#define FKV_PA_K 3
+#endif
+#ifndef FKV_PA_V
+#define FKV_PA_V 2
+#endif
+constexpr int kQStages = FKV_PA_Q;
 template <int D>
 struct PaCfg {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kTile = 128 * D * 2;
-  static constexpr int kStages = D == 128 ? 3 : 6;  // of K and of V
-  static constexpr uint32_t kOffK = kTile;
-  static constexpr uint32_t kOffV = kOffK + kStages * kTile;
-  static constexpr uint32_t kOffBar = kOffV + kStages * kTile;
+  static constexpr int kKStages = D == 128 ? FKV_PA_K : 6;
+  static constexpr int kVStages = D == 128 ? FKV_PA_V : 6;
+  static constexpr uint32_t kOffK = FKV_PA_Q * kTile;
+  static constexpr uint32_t kOffV = kOffK + kKStages * kTile;
+  static constexpr uint32_t kOffBar = kOffV + kVStages * kTile;
 };
 
 struct PaBars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[kQStages], q_empty[kQStages];
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t s_full[2], p_full[2];
   uint64_t o_ready, o_free, mma_done, x_full, x_read;
@@ -71,7 +82,7 @@ struct Streams {
 };
 
 // One operand of the key blocks, loaded by a whole warp.
-template <int D>
+template <int D, int kStages>
 __device__ __forceinline__ bool load_blocks(const PagedArgs& a, const Walk& w, const CUtensorMap* map,
                                             uint8_t* ring, uint64_t* full, uint64_t* empty,
                                             uint32_t& n, volatile int* abort) {
@@ -81,10 +92,10 @@ __device__ __forceinline__ bool load_blocks(const PagedArgs& a, const Walk& w, c
   const int my_page = lane / C::kHalves, my_half = lane % C::kHalves;
   const bool boxed = my_page * box_rows < 128;
   const int h = w.hm / a.mt;
-  const Streams st(w.steps());
+  const Streams st(w.count);
   auto key_of = [&](int i) {  // i: load order
     const int hh = i < 2 * st.nb1 ? i & 1 : 0, j = i < 2 * st.nb1 ? i >> 1 : i - st.nb1;
-    return block_at(w.t, w.j + st.step(hh, j)) * 128 + my_page * box_rows;
+    return block_at(w.t, w.first + st.step(hh, j)) * 128 + my_page * box_rows;
   };
   auto page_of = [&](int key) {
     if (!boxed || key >= w.s.kv) return -1;
@@ -96,7 +107,7 @@ __device__ __forceinline__ bool load_blocks(const PagedArgs& a, const Walk& w, c
   for (int i = 0; i < steps; ++i, ++n) {
     const int next_key = i + 1 < steps ? key_of(i + 1) : 0;
     const int next = i + 1 < steps ? page_of(next_key) : -1;
-    const uint32_t s = n % C::kStages, use = n / C::kStages;
+    const uint32_t s = n % kStages, use = n / kStages;
     if (!warp_wait(&empty[s], (use & 1) ^ 1, abort)) return false;
     const unsigned loads = __ballot_sync(0xffffffffu, id >= 0);
     if (lane == 0) {
@@ -120,7 +131,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
   using C = PaCfg<D>;
-  constexpr int kS = C::kStages;
+  constexpr int kKS = C::kKStages, kVS = C::kVStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {  // uniform: every thread sees the same base
     if (threadIdx.x == 0) {
@@ -135,11 +146,15 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
-    for (int s = 0; s < kS; ++s) {
+    for (int s = 0; s < kQStages; ++s) {
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 1);
+    }
+    for (int s = 0; s < kKS; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
+    }
+    for (int s = 0; s < kVS; ++s) {
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 1);
     }
@@ -175,27 +190,29 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
       const uint32_t q_bytes = uint32_t(a.mt == 1 ? a.tq * a.G : 128) * 128 * C::kHalves;
       uint32_t n = 0, u = 0;
       for (; !w.done(); w.next(a)) {
-        if (!warp_wait(&bars->q_empty, (u & 1) ^ 1, abort)) break;
+        const uint32_t qs = u % kQStages;
+        if (!warp_wait(&bars->q_empty[qs], ((u / kQStages) & 1) ^ 1, abort)) break;
         if (lane == 0) {
           const int h = w.hm / a.mt, m = w.hm - h * a.mt;
-          mbar_expect_tx(&bars->q_full, q_bytes);
+          mbar_expect_tx(&bars->q_full[qs], q_bytes);
           for (int half = 0; half < C::kHalves; ++half)
-            tma_load_3d(sm + half * kRegionBytes, &tm_q, &bars->q_full, half * 64,
-                        h * a.G + m * 128, w.s.q0 + w.qt * a.tq);
+            tma_load_3d(sm + qs * C::kTile + half * kRegionBytes, &tm_q, &bars->q_full[qs],
+                        half * 64, h * a.G + m * 128, w.s.q0 + w.qt * a.tq);
         }
         ++u;
-        if (!load_blocks<D>(a, w, &tm_k, sm + C::kOffK, bars->k_full, bars->k_empty, n, abort)) break;
+        if (!load_blocks<D, kKS>(a, w, &tm_k, sm + C::kOffK, bars->k_full, bars->k_empty, n, abort)) break;
       }
-      for (uint32_t i = n > kS ? n - kS : 0; i < n; ++i)
-        drain_wait(&bars->k_full[i % kS], (i / kS) & 1);
-      if (u > 0) drain_wait(&bars->q_full, (u - 1) & 1);
+      for (uint32_t i = n > kKS ? n - kKS : 0; i < n; ++i)
+        drain_wait(&bars->k_full[i % kKS], (i / kKS) & 1);
+      for (uint32_t i = u > kQStages ? u - kQStages : 0; i < u; ++i)
+        drain_wait(&bars->q_full[i % kQStages], (i / kQStages) & 1);
     } else if (warp == kPaV) {
       // ---------------------------------------------------------- V
       uint32_t n = 0;
       for (; !w.done(); w.next(a))
-        if (!load_blocks<D>(a, w, &tm_v, sm + C::kOffV, bars->v_full, bars->v_empty, n, abort)) break;
-      for (uint32_t i = n > kS ? n - kS : 0; i < n; ++i)
-        drain_wait(&bars->v_full[i % kS], (i / kS) & 1);
+        if (!load_blocks<D, kVS>(a, w, &tm_v, sm + C::kOffV, bars->v_full, bars->v_empty, n, abort)) break;
+      for (uint32_t i = n > kVS ? n - kVS : 0; i < n; ++i)
+        drain_wait(&bars->v_full[i % kVS], (i / kVS) & 1);
     } else if (warp == kPaMma && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t kIdQK = idesc_bf16(128, 128, false);
@@ -204,12 +221,13 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
       uint32_t uc = 0, ks = 0, kph = 0, vs = 0, vph = 0;
       uint32_t p_use[2] = {0, 0};
       bool ok = true;
-      const uint64_t dq = kmajor_desc(smem_u32(sm), 0);
+      const uint64_t dq0 = kmajor_desc(smem_u32(sm), 0);
       const uint64_t dk0 = kmajor_desc(smem_u32(sm + C::kOffK), 0);
       const uint64_t dv0 = mnmajor_desc(smem_u32(sm + C::kOffV), 0);
       for (; ok && !w.done(); w.next(a), ++uc) {
-        const Streams st(w.steps());
+        const Streams st(w.count);
         bool o_free_seen = false;
+        uint64_t dq = 0;
         auto issue_pv = [&](int h, bool first) -> bool {
           if (!o_free_seen) {
             if (!mbar_wait(&bars->o_free, (uc & 1) ^ 1, abort)) return false;
@@ -224,7 +242,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
           for (int k = 0; k < 8; ++k)  // 16 keys: 8 columns of P, 2048 B of V
             mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + k * 8, dv + uint64_t(k) * 128u, kIdPV,
                    (first && k == 0) ? 0u : 1u);
-          if (++vs == kS) { vs = 0; vph ^= 1; }
+          if (++vs == kVS) { vs = 0; vph ^= 1; }
           return true;
         };
         auto issue_s = [&](int h) -> bool {
@@ -236,10 +254,12 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
             mma_ss(tmem + 128u * h, dq + off, dk + off, kIdQK, k > 0 ? 1u : 0u);
           }
           mma_commit(&bars->s_full[h]);
-          if (++ks == kS) { ks = 0; kph ^= 1; }
+          if (++ks == kKS) { ks = 0; kph ^= 1; }
           return true;
         };
-        if (!(ok = mbar_wait(&bars->q_full, uc & 1, abort))) break;
+        const uint32_t qs = uc % kQStages;
+        dq = dq0 + uint64_t(qs * kStageDesc);
+        if (!(ok = mbar_wait(&bars->q_full[qs], (uc / kQStages) & 1, abort))) break;
         for (int j = 0; ok && j < st.nb0; ++j) {
           if (j > 0 && !(ok = issue_pv(0, j == 1))) break;
           if (!(ok = issue_s(0))) break;
@@ -251,7 +271,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
         }
         if (!ok) break;
-        mma_commit(&bars->q_empty);
+        mma_commit(&bars->q_empty[qs]);
         if (!(ok = issue_pv(0, st.nb0 == 1))) break;
         if (st.nb1 == st.nb0 && st.nb1 > 0 && !(ok = issue_pv(1, st.nb1 == 1))) break;
         mma_commit(&bars->o_ready);
@@ -271,7 +291,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
     uint32_t use = 0, base = 0, uc = 0;
     bool ok = true;
     for (; ok && !w.done(); w.next(a), ++uc) {
-      const Streams st(w.steps());
+      const Streams st(w.count);
       const int mine = st.count(h);
       int token, head;
       const bool valid = row_place(a, w.s, w.qt, w.hm, row, &token, &head);
@@ -285,14 +305,14 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
       const float slope = a.slopes && valid ? a.slopes[head] / a.scale : 0.f;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < mine; ++j, ++use) {
-        const int k0 = block_at(w.t, w.j + st.step(h, j)) * 128;
+        const int k0 = block_at(w.t, w.first + st.step(h, j)) * 128;
         if (!(ok = warp_wait(&bars->s_full[h], use & 1, abort))) break;
         tc_fence_after();
         if (row == 0) {
           // S_h(j) is complete, and every MMA issued before it: the K stage it
           // read and the V stage of this stream's previous PV are free
-          mbar_arrive(&bars->k_empty[(base + uint32_t(st.pos(h, j))) % kS]);
-          if (j > 0) mbar_arrive(&bars->v_empty[(base + uint32_t(st.pos(h, j - 1))) % kS]);
+          mbar_arrive(&bars->k_empty[(base + uint32_t(st.pos(h, j))) % kKS]);
+          if (j > 0) mbar_arrive(&bars->v_empty[(base + uint32_t(st.pos(h, j - 1))) % kVS]);
         }
         const bool full = k0 + 127 < w.s.pre || (k0 >= all_lo && k0 + 127 <= all_hi);
         if (live) {
@@ -374,8 +394,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
           const int key = k0 + row;
           const bool seen = key < w.s.pre || (key >= w.t.lo && key <= w.t.hi);
           if (__any_sync(0xffffffffu, !seen)) {
-            const uint32_t at = base + uint32_t(st.pos(h, j)), s = at % kS;
-            if (!(ok = warp_wait(&bars->v_full[s], (at / kS) & 1, abort))) break;
+            const uint32_t at = base + uint32_t(st.pos(h, j)), s = at % kVS;
+            if (!(ok = warp_wait(&bars->v_full[s], (at / kVS) & 1, abort))) break;
             if (!seen) {
               const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -393,7 +413,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
         mbar_arrive(&bars->p_full[h]);
       }
       if (!ok) break;
-      const uint32_t last_v = mine > 0 ? (base + uint32_t(st.pos(h, mine - 1))) % kS : 0u;
+      const uint32_t last_v = mine > 0 ? (base + uint32_t(st.pos(h, mine - 1))) % kVS : 0u;
       base += uint32_t(st.nb0 + st.nb1);
       // ---- merge the two streams; this thread takes D / 2 columns of its row
       if (!(ok = warp_wait(&bars->o_ready, uc & 1, abort))) break;
@@ -478,6 +498,7 @@ static cudaError_t launch_attend(PagedArgs a, cudaStream_t s) {
   a.mt = (a.G + 127) / 128;
   a.tq = a.mt == 1 ? 128 / a.G : 1;
   a.min_steps = 4;
+  a.extra = 3;
   CUtensorMap tq, tk, tv;
   if (!paged_tmaps(a, D, 128, a.mt == 1 ? a.G : 128, a.tq, &tq, &tk, &tv))
     return cudaErrorNotSupported;

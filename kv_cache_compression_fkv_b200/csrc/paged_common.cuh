@@ -8,15 +8,18 @@
 // token and a slice of R heads).  A unit costs as many steps as the key blocks
 // of TK keys that any of its rows can see; blocks that no row sees are never
 // loaded.  The units of the batch, ordered (sequence, query tile, head), laid
-// end to end make one line of steps that is cut into equal parts, one per CTA,
-// whatever the lengths are.  The cut is made on the GPU from cu_q, kv_len and
-// prefix_len, so a captured call stays valid when the lengths change.
+// end to end make one line that is cut into equal parts, one per CTA, whatever
+// the lengths are; on it a unit of n steps is n + `extra` long, `extra` (at its
+// head) standing for the time that a unit takes besides its steps.  The cut is
+// made on the GPU from cu_q, kv_len and prefix_len, so a captured call stays
+// valid when the lengths change.
 //
-// Join.  A unit cut by a part boundary is finished by paged_join_kernel from
-// the partial softmaxes (maximum, sum, unnormalised output, all fp32) of the
-// CTAs that share it.  A CTA leaves at most two: of its first unit (slot 0)
-// and of its last (slot 1).  They are merged in CTA order, so results do not
-// depend on timing.
+// Join.  A unit whose steps are cut by a part boundary is finished by
+// paged_join_kernel from the partial softmaxes (maximum, sum, unnormalised
+// output, all fp32) of the CTAs that share it.  A CTA leaves at most two: of a
+// unit that began in an earlier part (slot 0), and of the unit that goes on in
+// the next (slot 1).  They are merged in CTA order, so results do not depend on
+// timing.
 #pragma once
 
 #include <cuda.h>
@@ -39,6 +42,7 @@ struct PagedArgs : TileRule {
   int B, Hq;
   int page_shift, num_pages, max_pages, num_tokens;
   int min_steps;  // smallest part worth a CTA
+  int extra;      // what a unit costs besides its steps, in steps
   float scale, cap;
   // rows
   const void* q;
@@ -58,10 +62,10 @@ struct PagedArgs : TileRule {
 
 // Where a CTA's part of the line begins.
 struct PlanRec {
-  int b, qt, hm, j;  // sequence, query tile, head unit, step inside the unit
-  int n;             // steps of that unit
-  int per;           // steps per part
-  int count;         // steps of this part (0: none)
+  int b, qt, hm, j;  // sequence, query tile, head unit, place inside the unit
+  int n;             // length of that unit
+  int per;           // length of a part
+  int count;         // length of this part (0: none)
   int pad;
 };
 
@@ -95,12 +99,12 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
-// Steps of one sequence (one KV-head unit), computed by the whole warp.
-__device__ __forceinline__ int64_t seq_steps_warp(const PagedArgs& a, int b, int lane) {
+// Length of one sequence's units (of one KV head), computed by the whole warp.
+__device__ __forceinline__ int64_t seq_length_warp(const PagedArgs& a, int b, int lane) {
   const Seq s = load_seq(a, b);
   const int nq = query_tiles(a, s);
   int64_t w = 0;
-  for (int qt = lane; qt < nq; qt += 32) w += tile_span(a, s, qt).n;
+  for (int qt = lane; qt < nq; qt += 32) w += tile_span(a, s, qt).n + a.extra;
   return warp_sum(w);
 }
 
@@ -110,7 +114,7 @@ constexpr size_t kPlanScratch = sizeof(int64_t) * (32 + kMaxPagedSeqs + 1);
 template <int kThreads>
 __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, PlanRec* rec) {
   int64_t* warp_tot = scratch;     // [kThreads / 32]
-  int64_t* cum = scratch + 32;     // [B + 1] steps of the sequences before b
+  int64_t* cum = scratch + 32;     // [B + 1] length of the sequences before b
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hm_n = a.Hkv * a.mt;
   int64_t carry = 0;
@@ -124,14 +128,14 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
       const int nq = query_tiles(a, s);
       wide = nq > 2;
       if (!wide)
-        for (int qt = 0; qt < nq; ++qt) w += tile_span(a, s, qt).n;
+        for (int qt = 0; qt < nq; ++qt) w += tile_span(a, s, qt).n + a.extra;
     }
     // sequences of many query tiles are counted by the warp together
     unsigned todo = __ballot_sync(0xffffffffu, wide);
     while (todo) {
       const int src = __ffs(todo) - 1;
       todo &= todo - 1;
-      const int64_t t = seq_steps_warp(a, base + (warp << 5) + src, lane);
+      const int64_t t = seq_length_warp(a, base + (warp << 5) + src, lane);
       if (lane == src) w = t;
     }
     w *= hm_n;
@@ -176,7 +180,7 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
       int64_t rest = start - cum[lo];
       for (int q0 = 0; q0 < nq; q0 += 32) {
         const int qt = q0 + lane;
-        const int n = qt < nq ? tile_span(a, s, qt).n : 0;
+        const int n = qt < nq ? tile_span(a, s, qt).n + a.extra : 0;
         int64_t inc = int64_t(n) * hm_n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -186,7 +190,7 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
         const unsigned past = __ballot_sync(0xffffffffu, inc > rest);
         if (past) {
           const int src = __ffs(past) - 1;
-          const int64_t in_tile = rest - (inc - int64_t(n) * hm_n);  // lane src: steps into its tile
+          const int64_t in_tile = rest - (inc - int64_t(n) * hm_n);  // lane src: place in its tile
           const int64_t in = __shfl_sync(0xffffffffu, in_tile, src);
           r.n = __shfl_sync(0xffffffffu, n, src);
           r.qt = q0 + src;
@@ -205,45 +209,52 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
   __syncthreads();
 }
 
-// Walks the units of a part.  All roles of a CTA walk alike.
+// Walks the units of a part that have steps in it.  All roles of a CTA walk alike.
 struct Walk {
   Seq s;
   Span t;
-  int b, qt, hm, j, left, index;
+  int b, qt, hm;
+  int at, left;      // place inside the unit, what is left of the part
+  int first, count;  // steps of the unit in this part: first .. first + count - 1
 
   __device__ __forceinline__ void begin(const PagedArgs& a, const PlanRec& r) {
     b = r.b;
     qt = r.qt;
     hm = r.hm;
-    j = r.j;
+    at = r.j;
     left = r.count;
-    index = 0;
     if (left > 0) {
       s = load_seq(a, b);
       t = tile_span(a, s, qt);
+      cut(a);
+      if (count == 0) next(a);
     }
   }
   __device__ __forceinline__ bool done() const { return left <= 0; }
-  // Steps of the current unit that belong to this part.
-  __device__ __forceinline__ int steps() const { return t.n - j < left ? t.n - j : left; }
-  __device__ __forceinline__ bool whole() const { return j == 0 && left >= t.n; }
-  __device__ __forceinline__ int slot() const {
-    return 2 * int(blockIdx.x) + (index == 0 ? 0 : 1);
-  }
+  __device__ __forceinline__ bool whole() const { return first == 0 && count == t.n; }
+  __device__ __forceinline__ int slot() const { return 2 * int(blockIdx.x) + (first > 0 ? 0 : 1); }
   __device__ __forceinline__ void next(const PagedArgs& a) {
-    left -= steps();
-    ++index;
-    j = 0;
-    if (left <= 0) return;
-    if (++hm < a.Hkv * a.mt) return;
-    hm = 0;
-    if (++qt >= query_tiles(a, s)) {
-      qt = 0;
-      do {
-        s = load_seq(a, ++b);
-      } while (s.q_len == 0);
-    }
-    t = tile_span(a, s, qt);
+    do {
+      left -= t.n + a.extra - at;
+      if (left <= 0) return;
+      at = 0;
+      if (++hm >= a.Hkv * a.mt) {
+        hm = 0;
+        if (++qt >= query_tiles(a, s)) {
+          qt = 0;
+          do {
+            s = load_seq(a, ++b);
+          } while (s.q_len == 0);
+        }
+        t = tile_span(a, s, qt);
+      }
+      cut(a);
+    } while (count == 0);
+  }
+  __device__ __forceinline__ void cut(const PagedArgs& a) {
+    const int end = t.n + a.extra - at < left ? t.n + a.extra : at + left;
+    first = at > a.extra ? at - a.extra : 0;
+    count = end > a.extra ? end - a.extra - first : 0;
   }
 };
 

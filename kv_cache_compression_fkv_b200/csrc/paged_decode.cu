@@ -134,10 +134,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
           tma_load_3d(sm + C::kOffQ + (u & 1) * C::kQ + half * (kDecRows * 128), &tm_q,
                       &bars->q_full[u & 1], half * 64, h * a.G + m * kDecRows, w.s.q0);
       }
-      const int steps = w.steps();
+      const int steps = w.count;
       // this lane's page of step i (a bad id reads as zeros: a page past the end)
       auto page_of = [&](int i) {
-        const int key = block_at(w.t, w.j + i) * kDecKeys + my_page * box_rows;
+        const int key = block_at(w.t, w.first + i) * kDecKeys + my_page * box_rows;
         if (!boxed || key >= w.s.kv) return -1;
         const int id = page_id(a, w.b, key >> a.page_shift);
         return id < 0 ? (a.num_pages > 0 ? a.num_pages : 1) : id;
@@ -155,7 +155,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         __syncwarp();
         if (id >= 0) {
-          const int key = block_at(w.t, w.j + i) * kDecKeys + my_page * box_rows;
+          const int key = block_at(w.t, w.first + i) * kDecKeys + my_page * box_rows;
           tma_load_4d(sm + s * C::kStage + (my_v ? C::kOperand : 0) +
                           uint32_t(my_half) * (kDecKeys * 128) + uint32_t(my_page * box_rows) * 128,
                       map, &bars->full[s], my_half * 64, key & ((1 << a.page_shift) - 1), h, id);
@@ -199,13 +199,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (int i = 0; i < D / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-      const int steps = w.steps();
+      const int steps = w.count;
       uint32_t s = 0;
       for (int i = 0; i < steps; ++i, ++n) {
         s = n % C::kStages;
         if (!(ok = warp_wait(&bars->full[s], (n / C::kStages) & 1, abort))) break;
         const uint32_t k_addr = smem_u32(sm + s * C::kStage), v_addr = k_addr + C::kOperand;
-        const int k0 = block_at(w.t, w.j + i) * kDecKeys + warp * 16;  // this warp's keys
+        const int k0 = block_at(w.t, w.first + i) * kDecKeys + warp * 16;  // this warp's keys
         float x[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -405,6 +405,7 @@ static cudaError_t launch_decode(PagedArgs a, cudaStream_t s) {
   a.mt = (a.G + kDecRows - 1) / kDecRows;
   a.tq = 1;
   a.min_steps = 4;
+  a.extra = 1;
   CUtensorMap tq, tk, tv;
   if (!paged_tmaps(a, D, kDecKeys, kDecRows, 1, &tq, &tk, &tv)) return cudaErrorNotSupported;
   const size_t smem = 1024 + C::kOffBar + sizeof(DecBars);

@@ -18,14 +18,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   pdl_wait();
   const int c = int(blockIdx.x) + 1;
   const PlanRec r = a.rec[c];
-  // boundary c lies inside a unit, and the previous one does not
-  if (r.count == 0 || r.j == 0 || r.j > r.per) return;
+  // boundary c cuts the steps of a unit, and the previous one does not
+  if (r.count == 0 || r.j <= a.extra || r.j - r.per > a.extra) return;
   constexpr int kVec = D / 32;
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int parts = 1 + (r.n - r.j + r.per - 1) / r.per;
-  const int first_slot = 2 * (c - 1) + (r.j == r.per ? 0 : 1);
   const Seq s = load_seq(a, r.b);
   for (int row = blockIdx.y; row < a.R; row += gridDim.y) {
     int token, head;
@@ -34,7 +33,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
 #pragma unroll
     for (int v = 0; v < kVec; ++v) o[v] = 0.f;
     for (int i = warp; i < parts; i += kJoinWarps) {
-      const int64_t at = int64_t(i == 0 ? first_slot : 2 * (c - 1 + i)) * a.R + row;
+      const int64_t at = int64_t(i == 0 ? 2 * c - 1 : 2 * (c - 1 + i)) * a.R + row;
       const float2 ml = a.part_ml[at];
       float x[kVec];
       const float* src = a.part_o + at * D + lane * kVec;

@@ -53,9 +53,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
 #pragma unroll
       for (int v = 0; v < kDims; ++v) o[i][v] = 0.f;
     }
-    const int steps = w.steps();
+    const int steps = w.count;
     for (int i = 0; i < steps; ++i) {
-      const int k0 = block_at(w.t, w.j + i) * kSimtKeys;
+      const int k0 = block_at(w.t, w.first + i) * kSimtKeys;
       __syncthreads();
       // K and V rows of the tile; rows that no query of the tile sees, or that
       // lie in a bad page, are zeros, whatever the cache holds there
@@ -171,6 +171,7 @@ static cudaError_t launch_simt(PagedArgs a, cudaStream_t s) {
   a.mt = (a.G + R - 1) / R;
   a.tq = a.cu_q ? (a.mt == 1 ? R / a.G : 1) : 1;
   a.min_steps = 4;
+  a.extra = 1;
   const size_t plan = kPlanScratch;
   size_t smem = sizeof(float) * (R * D + kSimtKeys * (D + 4) + kSimtKeys * D);
   if (smem < plan) smem = plan;

@@ -150,11 +150,9 @@ def test_bad_pages_and_lengths_are_reported(cuda_device, dtype, op):
         s["kv_len"][1] = n
         run(s)
         assert status(s) == (7, 1)
-        rows = slice(0, case.q[0]), slice(sum(case.q[:2]), None)
-        ok = case.make()
-        run(ok)
-        for r in rows:
-            assert torch.equal(s["out"][r], ok["out"][r])
+        # against the oracle, not bit for bit: where the work is cut, and with it
+        # the order of the fp32 sums, goes by all lengths of the batch
+        check(case, s, only=(0, 2))
 
 
 def test_bad_token_offsets_are_reported(cuda_device):

@@ -483,8 +483,8 @@ int32_t fkv_step_fp8(const fkv_params_t* p, const fkv_step_io_t* io, const fkv_f
  * (ascending, cu_q[0] = 0), kv_len[b] the cached length of sequence b WITH the
  * tokens of this call, so that token i of the q_len = cu_q[b+1] - cu_q[b] new
  * ones has position kv_len[b] - q_len + i.  cu_q NULL: one token per sequence.
- * Rows of tokens at or behind cu_q[B] (a padded batch) are neither read nor
- * written.  num_tokens bounds the row arrays.
+ * Rows of tokens at or behind cu_q[B] (a padded batch) have no effect and are
+ * not written.  num_tokens bounds the row arrays.
  *
  * Every base pointer is 16-byte aligned and every stride a multiple of 16
  * bytes (strides of dimensions of size 1 are ignored).  Output rows must not

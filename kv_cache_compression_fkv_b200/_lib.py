@@ -131,17 +131,12 @@ SIGNATURES = {
                                           c_vp, c_vp, c_vp]),
     "fkv_step_fp8": (c_i32, [ctypes.POINTER(Params), ctypes.POINTER(StepIO), ctypes.POINTER(Fp8Cache),
                              c_vp, c_vp]),
-    "fkv_qk_norm_rope": (c_i32, [ctypes.POINTER(Rope), c_i32, c_i32, c_i32, c_i32, c_i32,
-                                 ctypes.POINTER(Rows), ctypes.POINTER(Rows), ctypes.POINTER(Rows),
-                                 ctypes.POINTER(Rows), c_vp]),
+    # structs by address: a byref() or the struct's bytes (paged.py packs them)
+    "fkv_qk_norm_rope": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "fkv_paged_workspace_size": (c_i32, [ctypes.POINTER(c_sz)]),
-    "fkv_paged_append": (c_i32, [ctypes.POINTER(Paged), ctypes.POINTER(Rope), c_i32,
-                                 ctypes.POINTER(Rows), ctypes.POINTER(Rows), ctypes.POINTER(Rows),
-                                 ctypes.POINTER(Rows), c_vp, c_vp]),
-    "fkv_paged_decode": (c_i32, [ctypes.POINTER(Paged), ctypes.POINTER(Rows), ctypes.POINTER(Rows),
-                                 c_vp, c_vp, c_vp]),
-    "fkv_paged_attend": (c_i32, [ctypes.POINTER(Paged), c_i32, ctypes.POINTER(Rows),
-                                 ctypes.POINTER(Rows), c_vp, c_vp, c_vp]),
+    "fkv_paged_append": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "fkv_paged_decode": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "fkv_paged_attend": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
 }
 
 _lib = None

@@ -3,9 +3,10 @@ append to the cache, and attention over it (include/fkv.h, "Paged cache").
 
 A :class:`Rope` and a :class:`PagedCache` are made once per model layer: they
 check the tensors that stay (weights, frequencies, caches, page table) and keep
-them alive.  The calls check and marshal the tensors of one step.  Every tensor
-of a call lives on the cache's device; the call runs there, on `stream` or on
-that device's current stream, whatever device is current.
+them alive.  The calls check and marshal the tensors of one step; a decoding
+step is short enough for that to count, so they pack the C structs as bytes.
+Every tensor of a call lives on the cache's device; the call runs there, on
+`stream` or on that device's current stream, whatever device is current.
 
 Nothing here is differentiable: these are serving operators, as the rest of
 the library.  Tensors used on another stream than the one they were allocated
@@ -13,9 +14,9 @@ on are the caller's to keep alive (``Tensor.record_stream``).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -23,53 +24,55 @@ import torch
 from . import _lib
 
 _DTYPES = {torch.bfloat16: _lib.FKV_DTYPE_BF16, torch.float32: _lib.FKV_DTYPE_FP32}
-_HERE = contextlib.nullcontext()
+_pack_rows = struct.Struct("=Qqq").pack     # fkv_rows_t
+_pack_batch = struct.Struct("=QQQ").pack    # kv_len, cu_q, prefix_len of fkv_paged_t
+_pack_places = struct.Struct("=Qq").pack    # positions, axis_stride of fkv_rope_t
 
 
-def _check(status: int, where: str):
+def _call(name: str, index: int, stream, *args):
+    """One library call on device `index`; its last argument is the stream."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != index:
+            raise ValueError(f"stream is on device {stream.device_index}, the call on device {index}")
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
+    fn = getattr(_lib.load(), name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
     if status != _lib.FKV_OK:
         from . import FkvError
-        raise FkvError(status, where)
+        raise FkvError(status, name)
 
 
-def _device(device: torch.device):
-    """The context in which a call on `device` runs."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _stream(stream, device: torch.device) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the call on {device}")
-        return stream.cuda_stream
-    return int(stream)
-
-
-def _vector(t: Optional[torch.Tensor], name: str, dtype, numel: int, device,
-            optional: bool = False) -> Optional[int]:
-    """Data pointer of a contiguous vector of at least numel entries."""
+def _vector(t: Optional[torch.Tensor], name: str, dtype, numel: int, index: int,
+            optional: bool = False) -> int:
+    """Data pointer of a contiguous vector of at least numel entries; 0 for None."""
     if t is None:
         if optional:
-            return None
+            return 0
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < numel:
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous() or t.numel() < numel:
         raise ValueError(f"{name} must be contiguous {dtype} with at least {numel} elements on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                         f"device {index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> _lib.Rows:
+def _rows(t: torch.Tensor, name: str, shape, dtype, index: int) -> bytes:
     """fkv_rows_t of a [tokens, heads, D] tensor whose last dimension is contiguous."""
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on device {index}, got {t.dtype} on {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     ts, hs, ds = t.stride()
     if ds != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return _lib.Rows(t.data_ptr(), ts, hs)
+    return _pack_rows(t.data_ptr(), ts, hs)
 
 
 class Rope:
@@ -80,40 +83,42 @@ class Rope:
         self.axis_pairs = tuple(int(n) for n in axis_pairs)
         if not 1 <= len(self.axis_pairs) <= 3:
             raise ValueError("axis_pairs has one to three entries")
-        n = sum(self.axis_pairs)
+        self._axes, self._pairs = len(self.axis_pairs), sum(self.axis_pairs)
         tensors = [t for t in (omega, q_weight, k_weight) if t is not None]
-        self.device = tensors[0].device if tensors else None
-        if self.device is not None and self.device.type != "cuda":
+        self._index = tensors[0].get_device() if tensors else None
+        if self._index is not None and self._index < 0:
             raise ValueError("omega and the weights must be CUDA tensors")
-        c = self._c = _lib.Rope()
+        # entries that the weights have; rows of that many dims and no more
+        self._dims = min([t.numel() for t in (q_weight, k_weight) if t is not None], default=1 << 30)
+        c = _lib.Rope()
         c.style = {"interleaved": _lib.FKV_ROPE_ADJACENT, "half": _lib.FKV_ROPE_HALF}[style]
         c.norm = 1 if norm else 0
-        c.n_axes = len(self.axis_pairs)
+        c.n_axes = self._axes
         for i, m in enumerate(self.axis_pairs):
             c.axis_pairs[i] = m
         c.eps = eps
-        c.omega = _vector(omega, "omega", torch.float32, n, self.device, optional=n == 0)
-        self._image = bytes(c)
+        for name in ("omega", "q_weight", "k_weight"):
+            setattr(c, name, _vector(getattr(self, name), name, torch.float32,
+                                     self._pairs if name == "omega" else 1, self._index,
+                                     optional=name != "omega" or self._pairs == 0) or None)
+        self._head = bytes(c)[:_lib.Rope.positions.offset]
 
-    def _call(self, head_dim, positions, tokens, device, cache_positions=False) -> _lib.Rope:
-        """The struct of one call."""
-        if self.device is not None and self.device != device:
-            raise ValueError(f"the rope's tensors are on {self.device}, the rows on {device}")
-        c = _lib.Rope.from_buffer_copy(self._image)
-        if self.q_weight is not None:
-            c.q_weight = _vector(self.q_weight, "q_weight", torch.float32, head_dim, device)
-        if self.k_weight is not None:
-            c.k_weight = _vector(self.k_weight, "k_weight", torch.float32, head_dim, device)
-        axes = len(self.axis_pairs)
-        if positions is not None:
-            shape = tuple(positions.shape)
-            if shape != (axes, tokens) and not (axes == 1 and shape == (tokens,)):
-                raise ValueError(f"positions must have the shape ({axes}, {tokens}), got {shape}")
-            c.positions = _vector(positions, "positions", torch.int32, axes * tokens, device)
-            c.axis_stride = tokens
-        elif sum(self.axis_pairs) > 0 and not (cache_positions and axes == 1):
-            raise ValueError("positions is required")
-        return c
+    def _struct(self, head_dim: int, positions, tokens: int, index: int,
+                cache_positions: bool = False) -> bytes:
+        """fkv_rope_t of one call."""
+        if self._index is not None and self._index != index:
+            raise ValueError(f"the rope's tensors are on device {self._index}, the rows on {index}")
+        if self._dims < head_dim:
+            raise ValueError(f"the weights have {self._dims} entries, the rows {head_dim} dims")
+        if positions is None:
+            if self._pairs > 0 and not (cache_positions and self._axes == 1):
+                raise ValueError("positions is required")
+            return self._head + _pack_places(0, 0)
+        shape = tuple(positions.shape)
+        if shape != (self._axes, tokens) and not (self._axes == 1 and shape == (tokens,)):
+            raise ValueError(f"positions must have the shape ({self._axes}, {tokens}), got {shape}")
+        return self._head + _pack_places(
+            _vector(positions, "positions", torch.int32, self._axes * tokens, index), tokens)
 
 
 def make_rope(omega: Optional[torch.Tensor] = None, *, axis_pairs: Optional[Sequence[int]] = None,
@@ -144,21 +149,20 @@ def qk_norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor
     some = q if q is not None else k
     if some is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q with q_out, k with k_out, or both pairs are required")
-    if some.dim() != 3 or some.dtype not in _DTYPES or not some.is_cuda:
+    dt, index = some.dtype, some.get_device()
+    if some.dim() != 3 or dt not in _DTYPES or index < 0:
         raise ValueError("rows are [tokens, heads, D] CUDA tensors in bfloat16 or float32")
-    dev, dt = some.device, some.dtype
     tokens, _, D = some.shape
-    hq = 0 if q is None else q.shape[1]
-    hk = 0 if k is None else k.shape[1]
-    rq, rqo = (None, None) if q is None else (_rows(q, "q", (tokens, hq, D), dt, dev),
-                                              _rows(q_out, "q_out", (tokens, hq, D), dt, dev))
-    rk, rko = (None, None) if k is None else (_rows(k, "k", (tokens, hk, D), dt, dev),
-                                              _rows(k_out, "k_out", (tokens, hk, D), dt, dev))
-    r = rope._call(D, positions, tokens, dev)
-    with _device(dev):
-        st = _lib.load().fkv_qk_norm_rope(r, _DTYPES[dt], D, tokens, hq, hk, rq, rk, rqo, rko,
-                                          _stream(stream, dev))
-    _check(st, "fkv_qk_norm_rope")
+    hq = hk = 0
+    rq = rqo = rk = rko = None
+    if q is not None:
+        hq = q.shape[1]
+        rq, rqo = _rows(q, "q", (tokens, hq, D), dt, index), _rows(q_out, "q_out", (tokens, hq, D), dt, index)
+    if k is not None:
+        hk = k.shape[1]
+        rk, rko = _rows(k, "k", (tokens, hk, D), dt, index), _rows(k_out, "k_out", (tokens, hk, D), dt, index)
+    _call("fkv_qk_norm_rope", index, stream, rope._struct(D, positions, tokens, index), _DTYPES[dt], D,
+          tokens, hq, hk, rq, rk, rqo, rko)
 
 
 class PagedCache:
@@ -192,6 +196,7 @@ class PagedCache:
         self.alibi_slopes, self.dtype = alibi_slopes, k_cache.dtype
         self.num_q_heads, self.num_seqs = int(num_q_heads), page_table.shape[0]
         self.num_kv_heads, self.head_dim = k_cache.shape[1], k_cache.shape[3]
+        self._index = k_cache.get_device()
         c = _lib.Paged()
         c.dtype = _DTYPES[self.dtype]
         c.flags = _lib.FKV_PAGED_CAUSAL if causal else 0
@@ -204,46 +209,36 @@ class PagedCache:
         c.table_stride = page_table.stride(0)
         c.k_cache, c.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
         c.page_table = page_table.data_ptr()
-        c.alibi_slopes = _vector(alibi_slopes, "alibi_slopes", torch.float32, self.num_q_heads, dev,
-                                 optional=True)
-        self._image = bytes(c)
+        c.alibi_slopes = _vector(alibi_slopes, "alibi_slopes", torch.float32, self.num_q_heads,
+                                 self._index, optional=True) or None
+        image = bytes(c)
+        self._head, self._tail = image[:_lib.Paged.kv_len.offset], image[_lib.Paged.alibi_slopes.offset:]
+        n = ctypes.c_size_t()
+        _lib.load().fkv_paged_workspace_size(ctypes.byref(n))
+        self._ws_bytes = n.value
 
     def workspace(self) -> torch.Tensor:
         """A zeroed workspace for calls on this device; one per stream of calls
         (calls that share a workspace must not overlap on the GPU)."""
-        n = ctypes.c_size_t()
-        _check(_lib.load().fkv_paged_workspace_size(ctypes.byref(n)), "fkv_paged_workspace_size")
-        with _device(self.device):
-            return torch.zeros(n.value, dtype=torch.uint8, device=self.device)
+        return torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
 
-    def _call(self, kv_len, cu_q=None, prefix_len=None) -> _lib.Paged:
-        """The struct of one call (a copy: calls from several threads do not share it)."""
-        c = _lib.Paged.from_buffer_copy(self._image)
-        c.kv_len = _vector(kv_len, "kv_len", torch.int32, self.num_seqs, self.device)
-        if cu_q is not None:
-            c.cu_q = _vector(cu_q, "cu_q", torch.int32, self.num_seqs + 1, self.device)
-        if prefix_len is not None:
-            c.prefix_len = _vector(prefix_len, "prefix_len", torch.int32, self.num_seqs, self.device)
-        return c
+    def _struct(self, kv_len, cu_q=None, prefix_len=None) -> bytes:
+        """fkv_paged_t of one call."""
+        n, index, i32 = self.num_seqs, self._index, torch.int32
+        return self._head + _pack_batch(
+            _vector(kv_len, "kv_len", i32, n, index),
+            0 if cu_q is None else _vector(cu_q, "cu_q", i32, n + 1, index),
+            0 if prefix_len is None else _vector(prefix_len, "prefix_len", i32, n, index)) + self._tail
+
+    def _rows(self, t, name, tokens, heads) -> bytes:
+        return _rows(t, name, (tokens, heads, self.head_dim), self.dtype, self._index)
 
     def _ws(self, ws) -> int:
-        n = _WS_BYTES or _workspace_bytes()
-        return _vector(ws, "ws", torch.uint8, n, self.device)
+        return _vector(ws, "ws", torch.uint8, self._ws_bytes, self._index)
 
-
-_WS_BYTES = 0
-
-
-def _workspace_bytes() -> int:
-    global _WS_BYTES
-    n = ctypes.c_size_t()
-    _check(_lib.load().fkv_paged_workspace_size(ctypes.byref(n)), "fkv_paged_workspace_size")
-    _WS_BYTES = n.value
-    return _WS_BYTES
-
-
-def _token_rows(t, name, cache: PagedCache, tokens, heads):
-    return _rows(t, name, (tokens, heads, cache.head_dim), cache.dtype, cache.device)
+    def _lse(self, lse, tokens) -> Optional[int]:
+        return None if lse is None else _vector(lse, "lse", torch.float32, tokens * self.num_q_heads,
+                                                self._index)
 
 
 def paged_append(cache: PagedCache, kv_len: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -259,21 +254,14 @@ def paged_append(cache: PagedCache, kv_len: torch.Tensor, k: torch.Tensor, v: to
     (which may be q) when given."""
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    tokens = k.shape[0]
-    c = cache._call(kv_len, cu_q)
-    rk = _token_rows(k, "k", cache, tokens, cache.num_kv_heads)
-    rv = _token_rows(v, "v", cache, tokens, cache.num_kv_heads)
-    rq = rqo = None
-    if q is not None:
-        rq = _token_rows(q, "q", cache, tokens, cache.num_q_heads)
-        rqo = _token_rows(q_out, "q_out", cache, tokens, cache.num_q_heads)
     if rope is None and positions is not None:
         raise ValueError("positions without a rope")
-    r = None if rope is None else rope._call(cache.head_dim, positions, tokens, cache.device, True)
-    with _device(cache.device):
-        st = _lib.load().fkv_paged_append(c, r, tokens, rq, rk, rv, rqo, cache._ws(ws),
-                                          _stream(stream, cache.device))
-    _check(st, "fkv_paged_append")
+    tokens, hk, hq = k.shape[0], cache.num_kv_heads, cache.num_q_heads
+    _call("fkv_paged_append", cache._index, stream, cache._struct(kv_len, cu_q),
+          None if rope is None else rope._struct(cache.head_dim, positions, tokens, cache._index, True), tokens,
+          None if q is None else cache._rows(q, "q", tokens, hq), cache._rows(k, "k", tokens, hk),
+          cache._rows(v, "v", tokens, hk), None if q is None else cache._rows(q_out, "q_out", tokens, hq),
+          cache._ws(ws))
 
 
 def paged_decode(cache: PagedCache, kv_len: torch.Tensor, q: torch.Tensor, out: torch.Tensor,
@@ -282,29 +270,20 @@ def paged_decode(cache: PagedCache, kv_len: torch.Tensor, q: torch.Tensor, out: 
     """Attention of one token per sequence, q and out [sequences, Hq, D], over
     the cached keys (fkv_paged_decode).  prefix_len: int32 [sequences], keys that
     every query sees whatever the window; lse: float32 [sequences, Hq] output."""
-    c = cache._call(kv_len, None, prefix_len)
-    n = cache.num_seqs
-    rq = _token_rows(q, "q", cache, n, cache.num_q_heads)
-    ro = _token_rows(out, "out", cache, n, cache.num_q_heads)
-    pl = _vector(lse, "lse", torch.float32, n * cache.num_q_heads, cache.device, optional=True)
-    with _device(cache.device):
-        st = _lib.load().fkv_paged_decode(c, rq, ro, pl, cache._ws(ws), _stream(stream, cache.device))
-    _check(st, "fkv_paged_decode")
+    n, hq = cache.num_seqs, cache.num_q_heads
+    _call("fkv_paged_decode", cache._index, stream, cache._struct(kv_len, None, prefix_len),
+          cache._rows(q, "q", n, hq), cache._rows(out, "out", n, hq), cache._lse(lse, n), cache._ws(ws))
 
 
-def paged_attend(cache: PagedCache, kv_len: torch.Tensor, cu_q: torch.Tensor, q: torch.Tensor,
-                 out: torch.Tensor, ws: torch.Tensor, *, prefix_len: Optional[torch.Tensor] = None,
-                 lse: Optional[torch.Tensor] = None, stream=None):
+def paged_attend(cache: PagedCache, kv_len: torch.Tensor, cu_q: Optional[torch.Tensor],
+                 q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *,
+                 prefix_len: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 stream=None):
     """Attention of a ragged batch of query tokens, q and out [tokens, Hq, D],
     over the cached keys (fkv_paged_attend); kv_len and cu_q as in
     :func:`paged_append`, prefix_len and lse (float32 [tokens, Hq]) as in
     :func:`paged_decode`."""
-    tokens = q.shape[0]
-    c = cache._call(kv_len, cu_q, prefix_len)
-    rq = _token_rows(q, "q", cache, tokens, cache.num_q_heads)
-    ro = _token_rows(out, "out", cache, tokens, cache.num_q_heads)
-    pl = _vector(lse, "lse", torch.float32, tokens * cache.num_q_heads, cache.device, optional=True)
-    with _device(cache.device):
-        st = _lib.load().fkv_paged_attend(c, tokens, rq, ro, pl, cache._ws(ws),
-                                          _stream(stream, cache.device))
-    _check(st, "fkv_paged_attend")
+    tokens, hq = q.shape[0], cache.num_q_heads
+    _call("fkv_paged_attend", cache._index, stream, cache._struct(kv_len, cu_q, prefix_len), tokens,
+          cache._rows(q, "q", tokens, hq), cache._rows(out, "out", tokens, hq), cache._lse(lse, tokens),
+          cache._ws(ws))

@@ -45,11 +45,11 @@ def _paged(**kw):
                 page_table=FAKE, kv_len=FAKE, cu_q=FAKE)
     for k, v in {**base, **kw}.items():
         setattr(c, k, v)
-    return c
+    return ctypes.byref(c)
 
 
 def _rows(ptr=FAKE, ts=8 * 128, hs=128):
-    return _lib.Rows(ptr, ts, hs)
+    return ctypes.byref(_lib.Rows(ptr, ts, hs))
 
 
 BAD = [
@@ -109,7 +109,7 @@ def test_nothing_to_do_is_no_error(lib):
     assert lib.fkv_paged_attend(_paged(), 0, None, None, None, FAKE, None) == 0
     assert lib.fkv_paged_decode(_paged(num_seqs=0, kv_len=None, page_table=None), None, None, None, FAKE, None) == 0
     assert lib.fkv_paged_append(_paged(), None, 0, None, None, None, None, FAKE, None) == 0
-    rope = _lib.Rope(n_axes=1)
+    rope = ctypes.byref(_lib.Rope(n_axes=1))
     assert lib.fkv_qk_norm_rope(rope, 0, 128, 0, 4, 4, None, None, None, None, None) == 0
     assert lib.fkv_qk_norm_rope(rope, 0, 128, 7, 0, 0, r, r, r, r, None) == 0
 
@@ -121,7 +121,7 @@ def _rope(**kw):
         r.axis_pairs[i] = n
     for k, v in kw.items():
         setattr(r, k, v)
-    return r
+    return ctypes.byref(r)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -170,11 +170,12 @@ def test_python_checks():
     meta = k.to("meta")
     with pytest.raises(ValueError):
         fkv.PagedCache(meta, meta, t, num_q_heads=4)
-    assert paged._rows(z((3, 2, 64), dtype=torch.bfloat16), "x", (3, 2, 64), torch.bfloat16,
-                       torch.device("cpu")).token_stride == 128
-    for bad in (z((3, 2, 64)), z((3, 64, 2), dtype=torch.bfloat16).transpose(1, 2), z((3, 1, 64), dtype=torch.bfloat16)):
+    packed = paged._rows(z((3, 2, 64), dtype=torch.bfloat16), "x", (3, 2, 64), torch.bfloat16, -1)
+    assert _lib.Rows.from_buffer_copy(packed).token_stride == 128
+    for bad in (z((3, 2, 64)), z((3, 64, 2), dtype=torch.bfloat16).transpose(1, 2), z((3, 1, 64), dtype=torch.bfloat16),
+                z((3, 2, 64), dtype=torch.bfloat16, device="meta")):
         with pytest.raises(ValueError):
-            paged._rows(bad, "x", (3, 2, 64), torch.bfloat16, torch.device("cpu"))
+            paged._rows(bad, "x", (3, 2, 64), torch.bfloat16, -1 if bad.device.type == "cpu" else 0)
 
 
 HARNESS = r"""

@@ -59,161 +59,221 @@ __device__ __forceinline__ uint4 repack(const float (&x)[4]) {
                     __float_as_uint(x[3]));
 }
 
-constexpr int kRowUnroll = 4;  // vectors that a thread has in flight
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
 
-// grid (tokens, slices of rows_per_cta rows); rows_per_cta * D / vector <=
-// kRowUnroll * blockDim.x, so every load of the CTA is issued before the
-// token's place and cosines are worked out.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a, int rows_per_cta) {
+// One new token of an append: where its key and value go.
+struct Place {
+  int64_t page_off;  // element offset of its cache row (head 0); -1: dropped
+  int pos;           // cache position
+  int live;          // 0: a padded row
+};
+
+__device__ __forceinline__ Place find_place(const RowsArgs& a, int t, int lane) {
+  Place p = {-1, 0, 0};
+  int b = t, i = 0, q_len = 1;
+  if (a.cu_q) {
+    b = find_seq(a.cu_q, a.B, t, lane);
+    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.tokens) {
+      if (lane == 0) report(a.status, FKV_ERR_DEVICE_ARG, b);
+      return p;
+    }
+    i = t - q0;
+    q_len = q1 - q0;
+    if (i < 0 || i >= q_len) return p;
+  }
+  p.live = 1;
+  const int cap = a.max_pages << a.page_shift;
+  int kv = a.kv_len[b];
+  bool bad = kv < 0 || kv > cap;
+  if (bad) kv = kv < 0 ? 0 : cap;
+  p.pos = kv - q_len + i;
+  int id = -1;
+  if (p.pos >= 0) id = a.page_table[int64_t(b) * a.table_stride + (p.pos >> a.page_shift)];
+  if (id >= 0 && id < a.num_pages)
+    p.page_off = int64_t(id) * a.page_stride + int64_t(p.pos & ((1 << a.page_shift) - 1)) * a.row_stride;
+  else
+    bad = true;
+  if (bad && lane == 0) report(a.status, FKV_ERR_DEVICE_ARG, b);
+  return p;
+}
+
+// A CTA takes kTok tokens and a slice of their rows.  Half as many threads as a
+// row has vectors share it: with half-split pairs a thread holds both halves of
+// its pairs (dims i .. and n + i ..), so the turn needs no exchange, one read of
+// the cosines serves two vectors, and the row's sum of squares one shuffle less.
+template <typename T, int D, int kTok>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a, int slice_rows) {
   constexpr int kVec = 16 / int(sizeof(T));  // elements per vector
-  constexpr int kLanes = D / kVec;           // lanes per row
-  __shared__ float2 cs[D / 2];
-  const int t = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int c = tid % kLanes, d0 = c * kVec;
-  const int pass = blockDim.x / kLanes;      // rows per pass of the CTA
+  constexpr int kChunks = D / kVec;          // vectors per row
+  constexpr int kTpr = kChunks / 2;          // threads per row
+  constexpr int kPass = kRowThreads / kTpr;  // rows per pass of the CTA
+  __shared__ __align__(16) float s_cos[kTok][D / 2], s_sin[kTok][D / 2];
+  __shared__ __align__(16) float s_w[2][D];
+  __shared__ Place s_place[kTok];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t0 = int(blockIdx.x) * kTok;
+  const int n_tok = kTok == 1 ? 1 : min(kTok, a.tokens - t0);
   const int n_rows = a.nq + a.nk + a.nv;
-  const int row0 = int(blockIdx.y) * rows_per_cta + tid / kLanes;
-  const int row1 = min(int(blockIdx.y + 1) * rows_per_cta, n_rows);
-  uint4 raw[kRowUnroll];
-#pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
-    const int row = row0 + u * pass;
-    if (row < row1) {
-      const T* src;
-      if (row < a.nq) src = static_cast<const T*>(a.q) + int64_t(t) * a.q_ts + int64_t(row) * a.q_hs;
-      else if (row < a.nq + a.nk)
-        src = static_cast<const T*>(a.k) + int64_t(t) * a.k_ts + int64_t(row - a.nq) * a.k_hs;
-      else
-        src = static_cast<const T*>(a.v) + int64_t(t) * a.v_ts + int64_t(row - a.nq - a.nk) * a.v_hs;
-      raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + d0));
+  const int first = int(blockIdx.y) * slice_rows;
+  const int rows = min(slice_rows, n_rows - first);  // of each token
+  const int total = rows * n_tok;
+  const int i = tid % kTpr;
+  // this thread's two vectors: the halves of its pairs, or neighbours
+  const int half_chunks = a.half ? a.pairs / kVec : 0;
+  const bool split = i < half_chunks;
+  const int ca = split ? i : 2 * i, cb = split ? i + half_chunks : 2 * i + 1;
+
+  auto source = [&](int t, int row) -> const T* {
+    if (row < a.nq) return static_cast<const T*>(a.q) + int64_t(t) * a.q_ts + int64_t(row) * a.q_hs;
+    row -= a.nq;
+    if (row < a.nk) return static_cast<const T*>(a.k) + int64_t(t) * a.k_ts + int64_t(row) * a.k_hs;
+    return static_cast<const T*>(a.v) + int64_t(t) * a.v_ts + int64_t(row - a.nk) * a.v_hs;
+  };
+  int item = tid / kTpr;  // (token, row) pair, rows innermost
+  int tok = item / rows, row = item - tok * rows;
+  uint4 ra, rb;
+  auto load = [&]() {
+    if (item < total) {
+      const T* src = source(t0 + tok, first + row);
+      ra = __ldcs(reinterpret_cast<const uint4*>(src + ca * kVec));
+      rb = __ldcs(reinterpret_cast<const uint4*>(src + cb * kVec));
     }
-  }
-  float wq[kVec], wk[kVec];
-#pragma unroll
-  for (int u = 0; u < kVec; ++u) wq[u] = wk[u] = 1.f;
-  if (a.norm) {
-#pragma unroll
-    for (int u = 0; u < kVec; ++u) {
-      if (a.q_weight) wq[u] = a.q_weight[d0 + u];
-      if (a.k_weight) wk[u] = a.k_weight[d0 + u];
-    }
-  }
-  int64_t page_off = -1;  // element offset of the token's cache row (head 0)
-  int pos = 0;
+  };
+  load();
+
   if (a.append) {
-    int b = t, i = 0, q_len = 1;
-    if (a.cu_q) {
-      b = find_seq(a.cu_q, a.B, t, lane);
-      const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
-      if (q0 < 0 || q1 < q0 || q1 > a.tokens) {
-        if (tid == 0) report(a.status, FKV_ERR_DEVICE_ARG, b);
-        return;
-      }
-      i = t - q0;
-      q_len = q1 - q0;
-      if (i < 0 || i >= q_len) return;  // a padded row
+    for (int k = warp; k < n_tok; k += kRowThreads / 32) {
+      const Place p = find_place(a, t0 + k, lane);
+      if (lane == 0) s_place[k] = p;
     }
-    const int cap = a.max_pages << a.page_shift;
-    int kv = a.kv_len[b];
-    if (kv < 0 || kv > cap) {
-      if (tid == 0) report(a.status, FKV_ERR_DEVICE_ARG, b);
-      kv = kv < 0 ? 0 : cap;
-    }
-    pos = kv - q_len + i;
-    int id = -1;
-    if (pos >= 0) id = a.page_table[int64_t(b) * a.table_stride + (pos >> a.page_shift)];
-    if (id >= 0 && id < a.num_pages)
-      page_off = int64_t(id) * a.page_stride +
-                 int64_t(pos & ((1 << a.page_shift) - 1)) * a.row_stride;
-    else if (tid == 0)
-      report(a.status, FKV_ERR_DEVICE_ARG, b);
   }
-  for (int i = tid; i < a.pairs; i += blockDim.x) {
-    const int axis = (i >= a.axis1) + (i >= a.axis2);
-    const int p = a.positions ? a.positions[axis * a.axis_stride + t] : pos;
-    const double turns = double(p) * (double(a.omega[i]) * 0.15915494309189535);
-    float sn, cn;
-    sincospif(2.f * float(turns - rint(turns)), &sn, &cn);
-    cs[i] = make_float2(cn, sn);
+  if (a.norm)
+    for (int k = tid; k < 2 * D; k += kRowThreads) {
+      const float* w = k < D ? a.q_weight : a.k_weight;
+      s_w[k >= D][k & (D - 1)] = w ? w[k & (D - 1)] : 1.f;
+    }
+  if (a.append) __syncthreads();
+  for (int k = tid; k < n_tok * a.pairs; k += kRowThreads) {
+    const int tk = kTok == 1 ? 0 : k / a.pairs, j = k - tk * a.pairs;
+    const int axis = (j >= a.axis1) + (j >= a.axis2);
+    const int p = a.positions ? a.positions[axis * a.axis_stride + t0 + tk] : s_place[tk].pos;
+    const double turns = double(p) * (double(a.omega[j]) * 0.15915494309189535);
+    sincospif(2.f * float(turns - rint(turns)), &s_sin[tk][j], &s_cos[tk][j]);
   }
   __syncthreads();
-  const unsigned group = kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
-#pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u) {
-    const int row = row0 + u * pass;
-    if (row >= row1) break;  // the lanes of a row leave together
-    const bool is_q = row < a.nq, is_v = row >= a.nq + a.nk;
+
+  const unsigned group = ((kTpr == 32 ? 0u : 1u << kTpr) - 1u) << (lane & ~(kTpr - 1));
+  while (item < total) {  // the threads of a row stay together
+    const uint4 xa = ra, xb = rb;
+    const int t = tok, r = first + row;
+    item += kPass;
+    row += kPass;
+    while (row >= rows) {
+      row -= rows;
+      ++tok;
+    }
+    load();
+    const bool is_q = r < a.nq, is_v = r >= a.nq + a.nk;
     T* dst;
-    if (is_q) dst = static_cast<T*>(a.q_out) + int64_t(t) * a.qo_ts + int64_t(row) * a.qo_hs;
-    else if (!a.append) dst = static_cast<T*>(a.k_out) + int64_t(t) * a.ko_ts + int64_t(row - a.nq) * a.ko_hs;
-    else {
-      if (page_off < 0) continue;
-      dst = is_v ? static_cast<T*>(a.v_cache) + page_off + int64_t(row - a.nq - a.nk) * a.head_stride
-                 : static_cast<T*>(a.k_cache) + page_off + int64_t(row - a.nq) * a.head_stride;
-    }
-    if (is_v) {
-      *reinterpret_cast<uint4*>(dst + d0) = raw[u];
-      continue;
-    }
-    float x[kVec];
-    unpack(raw[u], x);
-    if (a.norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-      const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) x[e] *= r * (is_q ? wq[e] : wk[e]);
-    }
-    if (a.half) {
-      // dims below n pair with dims n further (n a multiple of the vector)
-      const bool lo = d0 < a.pairs, turn = d0 < 2 * a.pairs;
-      const int other = (c + (lo ? 1 : -1) * (a.pairs / kVec)) & (kLanes - 1);
-      float y[kVec];
-#pragma unroll
-      for (int e = 0; e < kVec; ++e)
-        y[e] = __shfl_sync(group, x[e], (lane & ~(kLanes - 1)) | other);
-      if (turn) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float2 r = cs[(lo ? d0 : d0 - a.pairs) + e];
-          x[e] = lo ? x[e] * r.x - y[e] * r.y : y[e] * r.y + x[e] * r.x;
-        }
-      }
+    if (a.append && !s_place[t].live) continue;
+    if (is_q) {
+      dst = static_cast<T*>(a.q_out) + int64_t(t0 + t) * a.qo_ts + int64_t(r) * a.qo_hs;
+    } else if (!a.append) {
+      dst = static_cast<T*>(a.k_out) + int64_t(t0 + t) * a.ko_ts + int64_t(r - a.nq) * a.ko_hs;
     } else {
+      const int64_t off = s_place[t].page_off;
+      if (off < 0) continue;
+      dst = (is_v ? static_cast<T*>(a.v_cache) : static_cast<T*>(a.k_cache)) + off +
+            int64_t(is_v ? r - a.nq - a.nk : r - a.nq) * a.head_stride;
+    }
+    uint4 ya = xa, yb = xb;
+    if (!is_v) {
+      float x[2][kVec];
+      unpack(xa, x[0]);
+      unpack(xb, x[1]);
+      float2(&x2)[2][kVec / 2] = reinterpret_cast<float2(&)[2][kVec / 2]>(x);
+      if (a.norm) {
+        float2 s2 = mul2(x2[0][0], x2[0][0]);
 #pragma unroll
-      for (int e = 0; e < kVec; e += 2) {
-        const int i = (d0 + e) >> 1;
-        if (i < a.pairs) {
-          const float2 r = cs[i];
-          const float x0 = x[e], x1 = x[e + 1];
-          x[e] = x0 * r.x - x1 * r.y;
-          x[e + 1] = x0 * r.y + x1 * r.x;
+        for (int e = 1; e < kVec; ++e)
+          s2 = fma2(x2[e / (kVec / 2)][e % (kVec / 2)], x2[e / (kVec / 2)][e % (kVec / 2)], s2);
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = kTpr / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+        const float n = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        const float2 n2 = make_float2(n, n);
+        const float* w = s_w[is_q ? 0 : 1];
+#pragma unroll
+        for (int e = 0; e < kVec / 2; ++e) {
+          x2[0][e] = mul2(x2[0][e], mul2(n2, *reinterpret_cast<const float2*>(w + ca * kVec + 2 * e)));
+          x2[1][e] = mul2(x2[1][e], mul2(n2, *reinterpret_cast<const float2*>(w + cb * kVec + 2 * e)));
         }
       }
+      if (split) {  // pairs (ca + e, cb + e)
+#pragma unroll
+        for (int e = 0; e < kVec / 2; ++e) {
+          const float2 c = *reinterpret_cast<const float2*>(&s_cos[t][ca * kVec + 2 * e]);
+          const float2 s = *reinterpret_cast<const float2*>(&s_sin[t][ca * kVec + 2 * e]);
+          const float2 lo = x2[0][e], hi = x2[1][e];
+          x2[0][e] = fma2(lo, c, mul2(hi, make_float2(-s.x, -s.y)));
+          x2[1][e] = fma2(hi, c, mul2(lo, s));
+        }
+      } else if (!a.half) {  // adjacent pairs
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int p0 = (v ? cb : ca) * (kVec / 2);
+#pragma unroll
+          for (int e = 0; e < kVec / 2; ++e)
+            if (p0 + e < a.pairs) {
+              const float c = s_cos[t][p0 + e], s = s_sin[t][p0 + e];
+              const float lo = x[v][2 * e], hi = x[v][2 * e + 1];
+              x[v][2 * e] = lo * c - hi * s;
+              x[v][2 * e + 1] = lo * s + hi * c;
+            }
+        }
+      }
+      ya = repack(x[0]);
+      yb = repack(x[1]);
     }
-    *reinterpret_cast<uint4*>(dst + d0) = repack(x);
+    *reinterpret_cast<uint4*>(dst + ca * kVec) = ya;
+    *reinterpret_cast<uint4*>(dst + cb * kVec) = yb;
   }
 }
 
-cudaError_t launch_rows(const RowsArgs& a, bool bf16, int D, cudaStream_t s) {
+template <typename T, int D>
+static cudaError_t launch_rows_of(const RowsArgs& a, cudaStream_t s) {
+  constexpr int kPass = kRowThreads / (D * int(sizeof(T)) / 32);
   const int n_rows = a.nq + a.nk + a.nv;
-  if (a.tokens == 0 || n_rows == 0) return cudaSuccess;
-  const int lanes = D * (bf16 ? 2 : 4) / 16;
-  const int most = kRowUnroll * kRowThreads / lanes;  // rows that one CTA takes
-  const int slices = (n_rows + most - 1) / most;
-  const int rows_per_cta = (n_rows + slices - 1) / slices;
-  // 128 threads where they hold the rows in flight: more CTAs per SM, and fewer
-  // threads that wait for the token's cosines
-  const int threads = rows_per_cta * lanes <= kRowUnroll * 128 ? 128 : kRowThreads;
-  const dim3 grid(unsigned(a.tokens), unsigned(slices));
-  auto* k = bf16 ? (D == 128 ? rows_kernel<__nv_bfloat16, 128> : rows_kernel<__nv_bfloat16, 64>)
-                 : (D == 128 ? rows_kernel<float, 128> : rows_kernel<float, 64>);
-  return launch_kernel(k, grid, dim3(unsigned(threads)), 0, s, false, a, rows_per_cta);
+  // Many tokens: four per CTA, which share one search of their places and one
+  // round of cosines.  Few tokens: one pass of rows per CTA, for latency.
+  if (a.tokens >= 4 * 2 * num_sms())
+    return launch_kernel(rows_kernel<T, D, 4>, dim3(unsigned((a.tokens + 3) / 4)), dim3(kRowThreads), 0,
+                         s, false, a, n_rows);
+  const int slices = (n_rows + kPass - 1) / kPass;
+  return launch_kernel(rows_kernel<T, D, 1>, dim3(unsigned(a.tokens), unsigned(slices)),
+                       dim3(kRowThreads), 0, s, false, a, kPass);
+}
+
+cudaError_t launch_rows(const RowsArgs& a, bool bf16, int D, cudaStream_t s) {
+  if (a.tokens == 0 || a.nq + a.nk + a.nv == 0) return cudaSuccess;
+  if (bf16) return D == 128 ? launch_rows_of<__nv_bfloat16, 128>(a, s) : launch_rows_of<__nv_bfloat16, 64>(a, s);
+  return D == 128 ? launch_rows_of<float, 128>(a, s) : launch_rows_of<float, 64>(a, s);
 }
 
 }  // namespace fkv

@@ -15,7 +15,7 @@
 
 namespace fkv {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 64;
 
 // The sequence of token t: the last b with cu_q[b] <= t, found 32 ways at a
 // time by the warp (two rounds of loads for 1024 sequences).
@@ -113,161 +113,180 @@ __device__ __forceinline__ Place find_place(const RowsArgs& a, int t, int lane) 
   return p;
 }
 
-// A CTA takes kTok tokens and a slice of their rows.  Half as many threads as a
-// row has vectors share it: with half-split pairs a thread holds both halves of
-// its pairs (dims i .. and n + i ..), so the turn needs no exchange, one read of
-// the cosines serves two vectors, and the row's sum of squares one shuffle less.
-template <typename T, int D, int kTok>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a, int slice_rows) {
-  constexpr int kVec = 16 / int(sizeof(T));  // elements per vector
-  constexpr int kChunks = D / kVec;          // vectors per row
-  constexpr int kTpr = kChunks / 2;          // threads per row
-  constexpr int kPass = kRowThreads / kTpr;  // rows per pass of the CTA
-  __shared__ __align__(16) float s_cos[kTok][D / 2], s_sin[kTok][D / 2];
-  __shared__ __align__(16) float s_w[2][D];
-  __shared__ Place s_place[kTok];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t0 = int(blockIdx.x) * kTok;
-  const int n_tok = kTok == 1 ? 1 : min(kTok, a.tokens - t0);
-  const int n_rows = a.nq + a.nk + a.nv;
-  const int first = int(blockIdx.y) * slice_rows;
-  const int rows = min(slice_rows, n_rows - first);  // of each token
-  const int total = rows * n_tok;
-  const int i = tid % kTpr;
-  // this thread's two vectors: the halves of its pairs, or neighbours
-  const int half_chunks = a.half ? a.pairs / kVec : 0;
-  const bool split = i < half_chunks;
-  const int ca = split ? i : 2 * i, cb = split ? i + half_chunks : 2 * i + 1;
+// A warp takes one token and a run of its rows: the place, the cosines (two
+// pairs a lane) and the weights are then the warp's own, held in registers over
+// its rows, and no warp waits for another.  Half as many threads as a row has
+// vectors share it; with half-split pairs a thread holds both halves of its pairs
+// (dims i .. and n + i ..), so the turn needs no exchange.
+template <typename T, int D>
+struct RowTurn {
+  static constexpr int kVec = 16 / int(sizeof(T));  // elements per vector
+  static constexpr int kTpr = D / kVec / 2;         // threads per row
+  static constexpr int kStep = 32 / kTpr;           // rows per step of the warp
+  int da, db;       // first dims of this thread's two vectors
+  bool split;       // its pairs are (da + e, db + e)
+  int adjacent;     // its adjacent pairs that turn: bit e
+  float2 cs[kVec];  // (cosine, sine) of its pairs
+  float2 w[kVec];   // weights of da .., db ..
 
-  auto source = [&](int t, int row) -> const T* {
-    if (row < a.nq) return static_cast<const T*>(a.q) + int64_t(t) * a.q_ts + int64_t(row) * a.q_hs;
-    row -= a.nq;
-    if (row < a.nk) return static_cast<const T*>(a.k) + int64_t(t) * a.k_ts + int64_t(row) * a.k_hs;
-    return static_cast<const T*>(a.v) + int64_t(t) * a.v_ts + int64_t(row - a.nk) * a.v_hs;
-  };
-  int item = tid / kTpr;  // (token, row) pair, rows innermost
-  int tok = item / rows, row = item - tok * rows;
-  uint4 ra, rb;
-  auto load = [&]() {
-    if (item < total) {
-      const T* src = source(t0 + tok, first + row);
-      ra = __ldcs(reinterpret_cast<const uint4*>(src + ca * kVec));
-      rb = __ldcs(reinterpret_cast<const uint4*>(src + cb * kVec));
-    }
-  };
-  load();
-
-  if (a.append) {
-    for (int k = warp; k < n_tok; k += kRowThreads / 32) {
-      const Place p = find_place(a, t0 + k, lane);
-      if (lane == 0) s_place[k] = p;
+  __device__ __forceinline__ void weights(const float* src) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      const int d = (e < kVec / 2 ? da : db) + 2 * (e % (kVec / 2));
+      w[e] = src ? make_float2(src[d], src[d + 1]) : make_float2(1.f, 1.f);
     }
   }
-  if (a.norm)
-    for (int k = tid; k < 2 * D; k += kRowThreads) {
-      const float* w = k < D ? a.q_weight : a.k_weight;
-      s_w[k >= D][k & (D - 1)] = w ? w[k & (D - 1)] : 1.f;
+  __device__ __forceinline__ void row(uint4 (&y)[2], bool norm, float eps, unsigned group) const {
+    float x[2][kVec];
+    unpack(y[0], x[0]);
+    unpack(y[1], x[1]);
+    if (norm) {
+      float2(&x2)[kVec] = reinterpret_cast<float2(&)[kVec]>(x);
+      float2 s2 = mul2(x2[0], x2[0]);
+#pragma unroll
+      for (int e = 1; e < kVec; ++e) s2 = fma2(x2[e], x2[e], s2);
+      float ss = s2.x + s2.y;
+#pragma unroll
+      for (int o = kTpr / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+      const float n = rsqrtf(fmaf(ss, 1.f / D, eps));
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x2[e] = mul2(x2[e], mul2(make_float2(n, n), w[e]));
     }
-  if (a.append) __syncthreads();
-  for (int k = tid; k < n_tok * a.pairs; k += kRowThreads) {
-    const int tk = kTok == 1 ? 0 : k / a.pairs, j = k - tk * a.pairs;
-    const int axis = (j >= a.axis1) + (j >= a.axis2);
-    const int p = a.positions ? a.positions[axis * a.axis_stride + t0 + tk] : s_place[tk].pos;
-    const double turns = double(p) * (double(a.omega[j]) * 0.15915494309189535);
-    sincospif(2.f * float(turns - rint(turns)), &s_sin[tk][j], &s_cos[tk][j]);
-  }
-  __syncthreads();
-
-  const unsigned group = ((kTpr == 32 ? 0u : 1u << kTpr) - 1u) << (lane & ~(kTpr - 1));
-  while (item < total) {  // the threads of a row stay together
-    const uint4 xa = ra, xb = rb;
-    const int t = tok, r = first + row;
-    item += kPass;
-    row += kPass;
-    while (row >= rows) {
-      row -= rows;
-      ++tok;
-    }
-    load();
-    const bool is_q = r < a.nq, is_v = r >= a.nq + a.nk;
-    T* dst;
-    if (a.append && !s_place[t].live) continue;
-    if (is_q) {
-      dst = static_cast<T*>(a.q_out) + int64_t(t0 + t) * a.qo_ts + int64_t(r) * a.qo_hs;
-    } else if (!a.append) {
-      dst = static_cast<T*>(a.k_out) + int64_t(t0 + t) * a.ko_ts + int64_t(r - a.nq) * a.ko_hs;
+    if (split) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const float lo = x[0][e], hi = x[1][e];
+        x[0][e] = lo * cs[e].x - hi * cs[e].y;
+        x[1][e] = lo * cs[e].y + hi * cs[e].x;
+      }
     } else {
-      const int64_t off = s_place[t].page_off;
-      if (off < 0) continue;
-      dst = (is_v ? static_cast<T*>(a.v_cache) : static_cast<T*>(a.k_cache)) + off +
-            int64_t(is_v ? r - a.nq - a.nk : r - a.nq) * a.head_stride;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (adjacent & (1 << e)) {
+          float& lo = x[e / (kVec / 2)][2 * (e % (kVec / 2))];
+          float& hi = x[e / (kVec / 2)][2 * (e % (kVec / 2)) + 1];
+          const float l = lo, h = hi;
+          lo = l * cs[e].x - h * cs[e].y;
+          hi = l * cs[e].y + h * cs[e].x;
+        }
     }
-    uint4 ya = xa, yb = xb;
-    if (!is_v) {
-      float x[2][kVec];
-      unpack(xa, x[0]);
-      unpack(xb, x[1]);
-      float2(&x2)[2][kVec / 2] = reinterpret_cast<float2(&)[2][kVec / 2]>(x);
-      if (a.norm) {
-        float2 s2 = mul2(x2[0][0], x2[0][0]);
-#pragma unroll
-        for (int e = 1; e < kVec; ++e)
-          s2 = fma2(x2[e / (kVec / 2)][e % (kVec / 2)], x2[e / (kVec / 2)][e % (kVec / 2)], s2);
-        float ss = s2.x + s2.y;
-#pragma unroll
-        for (int o = kTpr / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-        const float n = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-        const float2 n2 = make_float2(n, n);
-        const float* w = s_w[is_q ? 0 : 1];
-#pragma unroll
-        for (int e = 0; e < kVec / 2; ++e) {
-          x2[0][e] = mul2(x2[0][e], mul2(n2, *reinterpret_cast<const float2*>(w + ca * kVec + 2 * e)));
-          x2[1][e] = mul2(x2[1][e], mul2(n2, *reinterpret_cast<const float2*>(w + cb * kVec + 2 * e)));
-        }
-      }
-      if (split) {  // pairs (ca + e, cb + e)
-#pragma unroll
-        for (int e = 0; e < kVec / 2; ++e) {
-          const float2 c = *reinterpret_cast<const float2*>(&s_cos[t][ca * kVec + 2 * e]);
-          const float2 s = *reinterpret_cast<const float2*>(&s_sin[t][ca * kVec + 2 * e]);
-          const float2 lo = x2[0][e], hi = x2[1][e];
-          x2[0][e] = fma2(lo, c, mul2(hi, make_float2(-s.x, -s.y)));
-          x2[1][e] = fma2(hi, c, mul2(lo, s));
-        }
-      } else if (!a.half) {  // adjacent pairs
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int p0 = (v ? cb : ca) * (kVec / 2);
-#pragma unroll
-          for (int e = 0; e < kVec / 2; ++e)
-            if (p0 + e < a.pairs) {
-              const float c = s_cos[t][p0 + e], s = s_sin[t][p0 + e];
-              const float lo = x[v][2 * e], hi = x[v][2 * e + 1];
-              x[v][2 * e] = lo * c - hi * s;
-              x[v][2 * e + 1] = lo * s + hi * c;
-            }
-        }
-      }
-      ya = repack(x[0]);
-      yb = repack(x[1]);
-    }
-    *reinterpret_cast<uint4*>(dst + ca * kVec) = ya;
-    *reinterpret_cast<uint4*>(dst + cb * kVec) = yb;
+    y[0] = repack(x[0]);
+    y[1] = repack(x[1]);
   }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a, int runs, int run_rows) {
+  using R = RowTurn<T, D>;
+  constexpr int kVec = R::kVec, kStep = R::kStep, kTpr = R::kTpr;
+  __shared__ float2 s_cs[kRowThreads / 32][D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t job = int64_t(blockIdx.x) * (kRowThreads / 32) + warp;
+  const int t = int(job / runs);
+  if (t >= a.tokens) return;
+  const int first = int(job - int64_t(t) * runs) * run_rows, end = first + run_rows;
+  const int i = lane % kTpr;
+  const int half_chunks = a.half ? a.pairs / kVec : 0;
+  R turn;
+  turn.split = i < half_chunks;
+  turn.da = (turn.split ? i : 2 * i) * kVec;
+  turn.db = (turn.split ? i + half_chunks : 2 * i + 1) * kVec;
+  turn.adjacent = 0;
+  Place place = {-1, 0, 1};
+  if (a.append) {
+    place = find_place(a, t, lane);
+    if (!place.live) return;
+  }
+  if (first < a.nq + a.nk && a.pairs > 0) {
+    for (int j = lane; j < a.pairs; j += 32) {
+      const int axis = (j >= a.axis1) + (j >= a.axis2);
+      const int p = a.positions ? a.positions[axis * a.axis_stride + t] : place.pos;
+      const double turns = double(p) * (double(a.omega[j]) * 0.15915494309189535);
+      float2 r;
+      sincospif(2.f * float(turns - rint(turns)), &r.y, &r.x);
+      s_cs[warp][j] = r;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      const int j = a.half ? turn.da + e : ((e < kVec / 2 ? turn.da : turn.db) >> 1) + e % (kVec / 2);
+      turn.cs[e] = j < a.pairs ? s_cs[warp][j] : make_float2(1.f, 0.f);
+      if (!a.half && j < a.pairs) turn.adjacent |= 1 << e;
+    }
+  }
+  const unsigned group = ((kTpr == 32 ? 0u : 1u << kTpr) - 1u) << (lane & ~(kTpr - 1));
+  // Rows [from, to) of one array, two steps of loads in flight.
+  auto pass = [&](const T* src, int64_t src_hs, T* dst, int64_t dst_hs, int from, int to, bool rotate) {
+    int r = from + lane / kTpr;
+    src += int64_t(r) * src_hs;
+    dst += int64_t(r) * dst_hs;
+    const int64_t src_step = kStep * src_hs, dst_step = kStep * dst_hs;
+    uint4 raw[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (r + u * kStep < to) {
+        raw[u][0] = __ldcs(reinterpret_cast<const uint4*>(src + turn.da));
+        raw[u][1] = __ldcs(reinterpret_cast<const uint4*>(src + turn.db));
+      }
+      src += src_step;
+    }
+    while (r < to) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (r >= to) break;  // the threads of a row leave together
+        uint4 y[2] = {raw[u][0], raw[u][1]};
+        if (r + 2 * kStep < to) {
+          raw[u][0] = __ldcs(reinterpret_cast<const uint4*>(src + turn.da));
+          raw[u][1] = __ldcs(reinterpret_cast<const uint4*>(src + turn.db));
+        }
+        if (rotate) turn.row(y, a.norm, a.eps, group);
+        *reinterpret_cast<uint4*>(dst + turn.da) = y[0];
+        *reinterpret_cast<uint4*>(dst + turn.db) = y[1];
+        r += kStep;
+        src += src_step;
+        dst += dst_step;
+      }
+    }
+  };
+  if (first < a.nq) {
+    if (a.norm) turn.weights(a.q_weight);
+    pass(static_cast<const T*>(a.q) + int64_t(t) * a.q_ts, a.q_hs,
+         static_cast<T*>(a.q_out) + int64_t(t) * a.qo_ts, a.qo_hs, first, min(end, a.nq), true);
+  }
+  if (a.append && place.page_off < 0) return;
+  const int k0 = max(first - a.nq, 0), k1 = min(end - a.nq, a.nk);
+  if (k0 < k1) {
+    if (a.norm) turn.weights(a.k_weight);
+    T* dst = a.append ? static_cast<T*>(a.k_cache) + place.page_off
+                      : static_cast<T*>(a.k_out) + int64_t(t) * a.ko_ts;
+    pass(static_cast<const T*>(a.k) + int64_t(t) * a.k_ts, a.k_hs, dst,
+         a.append ? a.head_stride : a.ko_hs, k0, k1, true);
+  }
+  const int v0 = max(first - a.nq - a.nk, 0), v1 = min(end - a.nq - a.nk, a.nv);
+  if (v0 < v1)
+    pass(static_cast<const T*>(a.v) + int64_t(t) * a.v_ts, a.v_hs,
+         static_cast<T*>(a.v_cache) + place.page_off, a.head_stride, v0, v1, false);
 }
 
 template <typename T, int D>
 static cudaError_t launch_rows_of(const RowsArgs& a, cudaStream_t s) {
-  constexpr int kPass = kRowThreads / (D * int(sizeof(T)) / 32);
+  constexpr int kStep = 32 / (D * int(sizeof(T)) / 32);
+  constexpr int kWarps = kRowThreads / 32;
   const int n_rows = a.nq + a.nk + a.nv;
-  // Many tokens: four per CTA, which share one search of their places and one
-  // round of cosines.  Few tokens: one pass of rows per CTA, for latency.
-  if (a.tokens >= 4 * 2 * num_sms())
-    return launch_kernel(rows_kernel<T, D, 4>, dim3(unsigned((a.tokens + 3) / 4)), dim3(kRowThreads), 0,
-                         s, false, a, n_rows);
-  const int slices = (n_rows + kPass - 1) / kPass;
-  return launch_kernel(rows_kernel<T, D, 1>, dim3(unsigned(a.tokens), unsigned(slices)),
-                       dim3(kRowThreads), 0, s, false, a, kPass);
+  // Runs as long as the token's rows, or shorter where there are few tokens, down
+  // to one step each, so that about 16 warps per SM share the rows.
+  const int64_t want = int64_t(16) * num_sms();
+  int64_t runs = (want + a.tokens - 1) / a.tokens;
+  const int64_t most = (n_rows + kStep - 1) / kStep;
+  if (runs > most) runs = most;
+  int run_rows = int((n_rows + runs - 1) / runs);
+  run_rows = (run_rows + kStep - 1) / kStep * kStep;
+  runs = (n_rows + run_rows - 1) / run_rows;
+  const int64_t jobs = int64_t(a.tokens) * runs;
+  const int64_t ctas = (jobs + kWarps - 1) / kWarps;
+  if (ctas > int64_t(0x7fffffff)) return cudaErrorInvalidConfiguration;
+  return launch_kernel(rows_kernel<T, D>, dim3(unsigned(ctas)), dim3(kRowThreads), 0, s, false, a,
+                       int(runs), run_rows);
 }
 
 cudaError_t launch_rows(const RowsArgs& a, bool bf16, int D, cudaStream_t s) {

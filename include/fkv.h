@@ -487,8 +487,10 @@ int32_t fkv_step_fp8(const fkv_params_t* p, const fkv_step_io_t* io, const fkv_f
  * not written.  num_tokens bounds the row arrays.
  *
  * Every base pointer is 16-byte aligned and every stride a multiple of 16
- * bytes (strides of dimensions of size 1 are ignored).  Output rows must not
- * overlap one another or any input, except where an entry point says so.
+ * bytes, at most 2^37 elements (strides of dimensions of size 1 are ignored).
+ * A stride of input rows may be 0 (shared rows), but for the queries of an
+ * attention.  Output rows must not overlap one another or any input, except
+ * where an entry point says so.
  * bf16 or fp32 throughout (dtype); D is 64 or 128; page_size is a power of
  * two, 8 .. 1024; at most 8192 sequences, max_pages * page_size <= 2^30, and
  * fewer than 2^31 tokens.

@@ -16,7 +16,7 @@ int32_t launch_status(cudaError_t e) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-const int64_t kMaxStride = int64_t(1) << 38;  // elements; tensor maps end at 2^40 bytes
+const int64_t kMaxStride = int64_t(1) << 37;  // elements; tensor maps end at 2^40 bytes
 
 // Row strides as the kernels use them: 0 where the dimension has one entry.
 struct Strides {
@@ -176,6 +176,8 @@ int32_t attention(const fkv_paged_t* c, int64_t tokens, bool single, const fkv_r
   if ((st = check_rows(q, tokens, a.Hq, c->head_dim, elem, false, &sq)) != FKV_OK) return st;
   if ((st = check_rows(out, tokens, a.Hq, c->head_dim, elem, true, &so)) != FKV_OK) return st;
   if (!aligned(lse, 4)) return FKV_ERR_INVALID_ARG;
+  // tensor maps have no zero strides
+  if (tokens > 0 && ((a.Hq > 1 && sq.hs == 0) || (tokens > 1 && sq.ts == 0))) return FKV_ERR_SHAPE;
   if (!single && !c->cu_q && tokens != c->num_seqs) return FKV_ERR_SHAPE;
   if ((st = check_paged_ws(ws, &a)) != FKV_OK) return st;
   if (tokens == 0 || c->num_seqs == 0) return FKV_OK;
@@ -188,9 +190,7 @@ int32_t attention(const fkv_paged_t* c, int64_t tokens, bool single, const fkv_r
   a.o_ts = so.ts;
   a.o_hs = so.hs;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (c->dtype == FKV_DTYPE_FP32) return launch_status(launch_paged_simt(a, c->head_dim, s));
-  // tensor maps have no zero strides
-  if ((a.Hq > 1 && a.q_hs == 0) || (tokens > 1 && a.q_ts == 0)) return FKV_ERR_SHAPE;
+  if (c->dtype == FKV_DTYPE_FP32) return launch_status(launch_paged_f32(a, c->head_dim, s));
   if (single) return launch_status(launch_paged_decode(a, c->head_dim, s));
   return launch_status(launch_paged_attend(a, c->head_dim, s));
 }

@@ -500,7 +500,7 @@ static cudaError_t launch_attend(PagedArgs a, cudaStream_t s) {
   a.min_steps = 4;
   a.extra = 3;
   CUtensorMap tq, tk, tv;
-  if (!paged_tmaps(a, D, 128, a.mt == 1 ? a.G : 128, a.tq, &tq, &tk, &tv))
+  if (!paged_tmaps(a, D, true, 128, a.mt == 1 ? a.G : 128, a.tq, &tq, &tk, &tv))
     return cudaErrorNotSupported;
   const size_t smem = C::kOffBar + sizeof(PaBars);
   static_assert(C::kOffBar + sizeof(PaBars) <= 232448, "above the per-CTA limit");

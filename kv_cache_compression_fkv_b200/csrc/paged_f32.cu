@@ -1,0 +1,353 @@
+// Paged attention in fp32 (the library's accuracy mode) on the CUDA cores, one
+// kernel for single tokens and for chunks: fp32 products and sums throughout.
+//
+// The four warps of a CTA stream 32-key blocks of K and V through a ring filled
+// with 16-byte asynchronous copies (rows that no query sees, or of a bad page, are
+// filled with zeros, whatever the cache holds there).  Each warp takes 8 keys of
+// every block: four lanes share a key and split its dims for the scores of all R
+// rows, then lane (key, row) holds one score, so the softmax step is three
+// shuffles; for P V a lane owns D / 32 output dims.  Every warp keeps the running
+// maximum, sum and output of the R rows for its keys, so the warps meet once per
+// block (for the ring) and join at the end of a unit.
+// R = 4 for single tokens of up to four query heads per KV head: per 32 KB block
+// (D = 128) about 350 issue slots a scheduler, a quarter of what HBM leaves.  R =
+// 16 otherwise: a chunk packs 16 (token, head) rows, bound by the FMA pipe and
+// the broadcast reads of Q (20 shared-memory wavefronts per 64 FMAs of a warp).
+#include "paged_common.cuh"
+
+namespace fkv {
+
+constexpr int kF32Threads = 128;
+constexpr int kF32Keys = 32;
+
+template <int D, int R>
+struct F32Cfg {
+  static constexpr int kPitch = D + 16;  // floats per K row: 8 rows x 64 B without conflicts
+  static constexpr int kK = kF32Keys * kPitch, kV = kF32Keys * D;
+  static constexpr int kStages = D == 128 && R == 16 ? 2 : 3;
+  static constexpr int kQ = R * D;                         // one slot per stage
+  static constexpr int kStage = kK + kV + kQ;              // floats
+  static constexpr int kOffP = kStages * kStage;           // [32 keys][R]
+  static constexpr int kOffO = kOffP + kF32Keys * R;       // [2][R][D]
+  static constexpr int kOffMl = kOffO + 2 * R * D;         // [2][R] float2
+  static constexpr int kFloats = kOffMl + 2 * R * 2;
+};
+
+__device__ __forceinline__ void cp_async16(float* dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(read ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Starts the copies of step i of a unit into a stage, and of the unit's queries
+// with its first step.
+template <int D, int R>
+__device__ __forceinline__ void load_step(const PagedArgs& a, const Walk& w, int i, float* stage) {
+  using C = F32Cfg<D, R>;
+  constexpr int kChunks = D / 4;  // 16-byte chunks per row
+  const int h = w.hm / a.mt;
+  const int k0 = block_at(w.t, w.first + i) * kF32Keys;
+  const float* kc = static_cast<const float*>(a.k_cache) + int64_t(h) * a.head_stride;
+  const float* vc = static_cast<const float*>(a.v_cache) + int64_t(h) * a.head_stride;
+  constexpr int kPass = kF32Threads / kChunks;  // rows per pass
+  const int c = (threadIdx.x % kChunks) * 4;
+#pragma unroll
+  for (int p = 0; p < kF32Keys / kPass; ++p) {
+    const int r = p * kPass + threadIdx.x / kChunks, j = k0 + r;
+    bool read = j < w.s.kv && (j < w.s.pre || (j >= w.t.lo && j <= w.t.hi));
+    int64_t off = 0;
+    if (read) {
+      const int id = page_id(a, w.b, j >> a.page_shift);
+      read = id >= 0;
+      if (read)
+        off = int64_t(id) * a.page_stride + int64_t(j & ((1 << a.page_shift) - 1)) * a.row_stride;
+    }
+    const float* none = static_cast<const float*>(a.q);  // an address to name when nothing is read
+    cp_async16(stage + r * C::kPitch + c, read ? kc + off + c : none, read);
+    cp_async16(stage + C::kK + r * D + c, read ? vc + off + c : none, read);
+  }
+  if (i == 0) {
+    float* Q = stage + C::kK + C::kV;
+#pragma unroll
+    for (int p = 0; p < (R + kPass - 1) / kPass; ++p) {
+      const int r = p * kPass + threadIdx.x / kChunks;
+      if (r < R) {
+        int token, head;
+        const bool read = row_place(a, w.s, w.qt, w.hm, r, &token, &head);
+        const float* src = static_cast<const float*>(a.q);
+        if (read) src += int64_t(w.s.q0 + token) * a.q_ts + int64_t(head) * a.q_hs + c;
+        cp_async16(Q + r * D + c, src, read);
+      }
+    }
+  }
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedArgs a) {
+  using C = F32Cfg<D, R>;
+  constexpr int kDims = D / 32;  // output dims per lane
+  constexpr int kGroups = R / 4;
+  extern __shared__ __align__(16) float sm[];
+  __shared__ PlanRec rec;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  plan_part<kF32Threads>(a, reinterpret_cast<int64_t*>(sm), &rec);
+  const float kLog2e = 1.4426950408889634f;
+  float* P = sm + C::kOffP;
+  float* O = sm + C::kOffO;
+  float2* ML = reinterpret_cast<float2*>(sm + C::kOffMl);
+  // this lane's key inside a block, and its dims quarter (scores) or row in each
+  // group of four (softmax)
+  const int key = warp * 8 + (lane >> 2), sub = lane & 3;
+
+  // the loads run kStages - 1 steps ahead, over the ends of units
+  Walk lw, w;
+  lw.begin(a, rec);
+  w.begin(a, rec);
+  int li = 0, ln = 0;
+  auto load_next = [&]() {
+    if (!lw.done()) {
+      load_step<D, R>(a, lw, li, sm + (ln % C::kStages) * C::kStage);
+      ++ln;
+      if (++li == lw.count) {
+        li = 0;
+        lw.next(a);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < C::kStages - 1; ++s) load_next();
+
+  int n = 0;
+  for (; !w.done(); w.next(a)) {
+    const int h = w.hm / a.mt, m0 = (w.hm - h * a.mt) * R;
+    const int p0 = w.s.kv - w.s.q_len + w.qt * a.tq;  // position of the first token
+    const int all_hi = a.causal ? p0 : w.s.kv - 1;
+    const int all_lo = a.window > 0 ? p0 + a.tq - a.window : 0;
+    // rows 4 g + sub: position, span and slope
+    int pos[kGroups];
+    float slope[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int r = 4 * g + sub;
+      const int i = a.mt == 1 ? r % a.G : m0 + r;
+      pos[g] = p0 + (a.mt == 1 ? r / a.G : 0);
+      slope[g] = a.slopes && i < a.G ? a.slopes[h * a.G + i] : 0.f;
+    }
+    float m[kGroups], l[kGroups], o[R][kDims];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      m[g] = -INFINITY;
+      l[g] = 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[r][d] = 0.f;
+    // the queries stay in the stage of the unit's first step: keep a copy
+    float* Qs = O;  // free between joins: [R][D] of its 2 R D floats
+    for (int i = 0; i < w.count; ++i, ++n) {
+      cp_async_wait<C::kStages - 2>();
+      __syncthreads();  // step n is here for all; step n - 1 is done with
+      float* stage = sm + (n % C::kStages) * C::kStage;
+      load_next();
+      const float* Q = i == 0 ? stage + C::kK + C::kV : Qs;
+      const int k0 = block_at(w.t, w.first + i) * kF32Keys, j = k0 + key;
+      float z[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) z[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int d = (4 * c + sub) * 4;
+        const float4 k4 = *reinterpret_cast<const float4*>(stage + key * C::kPitch + d);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 q4 = *reinterpret_cast<const float4*>(Q + r * D + d);
+          z[r] = fmaf(q4.x, k4.x, z[r]);
+          z[r] = fmaf(q4.y, k4.y, z[r]);
+          z[r] = fmaf(q4.z, k4.z, z[r]);
+          z[r] = fmaf(q4.w, k4.w, z[r]);
+        }
+      }
+      const bool full = k0 + 31 < w.s.pre || (k0 >= all_lo && k0 + 31 <= all_hi);
+      float corr[kGroups];
+      bool grew = false;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        // four dot products over four lanes: lane `sub` ends with row 4 g + sub
+        float u = sub & 1 ? z[4 * g] : z[4 * g + 1], v = sub & 1 ? z[4 * g + 2] : z[4 * g + 3];
+        u = __shfl_xor_sync(0xffffffffu, u, 1);
+        v = __shfl_xor_sync(0xffffffffu, v, 1);
+        const float s01 = (sub & 1 ? z[4 * g + 1] : z[4 * g]) + u;
+        const float s23 = (sub & 1 ? z[4 * g + 3] : z[4 * g + 2]) + v;
+        const float t = __shfl_xor_sync(0xffffffffu, sub & 2 ? s01 : s23, 2);
+        float x = ((sub & 2 ? s23 : s01) + t) * a.scale;
+        if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
+        if (a.slopes) x = fmaf(slope[g], float(j - pos[g]), x);
+        x *= kLog2e;
+        if (!full) {
+          const RowSpan rs = row_span(a, w.s, pos[g]);
+          if (!(j < w.s.kv && (j < w.s.pre || (j >= rs.lo && j <= rs.hi)))) x = -INFINITY;
+        }
+        float mx = x;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m[g], mx);
+        const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen so far
+        corr[g] = exp2_fast(m[g] - ms);
+        grew |= mn > m[g];
+        const float p = exp2_fast(x - ms);
+        l[g] = l[g] * corr[g] + p;
+        m[g] = mn;
+        P[key * R + 4 * g + sub] = p;
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float f = __shfl_sync(0xffffffffu, corr[r / 4], r & 3);
+#pragma unroll
+          for (int d = 0; d < kDims; ++d) o[r][d] *= f;
+        }
+      }
+      __syncwarp();
+      const float* V = stage + C::kK + lane * kDims;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float vv[kDims];
+#pragma unroll
+        for (int d = 0; d < kDims; d += 2)
+          *reinterpret_cast<float2*>(&vv[d]) =
+              *reinterpret_cast<const float2*>(V + (warp * 8 + k) * D + d);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const float4 p = *reinterpret_cast<const float4*>(P + (warp * 8 + k) * R + 4 * g);
+#pragma unroll
+          for (int d = 0; d < kDims; ++d) {
+            o[4 * g][d] = fmaf(p.x, vv[d], o[4 * g][d]);
+            o[4 * g + 1][d] = fmaf(p.y, vv[d], o[4 * g + 1][d]);
+            o[4 * g + 2][d] = fmaf(p.z, vv[d], o[4 * g + 2][d]);
+            o[4 * g + 3][d] = fmaf(p.w, vv[d], o[4 * g + 3][d]);
+          }
+        }
+      }
+      if (i == 0 && w.count > 1) {
+        // before the stage is loaded again, which is after the next barrier at
+        // the earliest; read after that barrier too
+#pragma unroll
+        for (int e = threadIdx.x * 4; e < R * D; e += kF32Threads * 4)
+          *reinterpret_cast<float4*>(Qs + e) = *reinterpret_cast<const float4*>(Q + e);
+      }
+      __syncwarp();  // P is read by all lanes before the next block's is written
+    }
+    // ---- join the warps: 2, 3 into 0, 1, then 1 into 0
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], off);
+#pragma unroll
+    for (int half = 2; half; half >>= 1) {
+      __syncthreads();  // the queries' copy, or the slot of the round before, is read
+      if (warp >= half && warp < 2 * half) {
+        float* dst = O + (warp - half) * R * D + lane * kDims;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int d = 0; d < kDims; d += 2)
+            *reinterpret_cast<float2*>(dst + r * D + d) = make_float2(o[r][d], o[r][d + 1]);
+        if (lane < 4)
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+            ML[(warp - half) * R + 4 * g + lane] = make_float2(m[g], l[g]);
+      }
+      __syncthreads();
+      if (warp < half) {
+        const float* src = O + warp * R * D + lane * kDims;
+        float ca[kGroups], cb[kGroups];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const float2 t = ML[warp * R + 4 * g + sub];
+          const float mn = fmaxf(m[g], t.x), ms = mn == -INFINITY ? 0.f : mn;
+          ca[g] = exp2_fast(m[g] - ms);
+          cb[g] = exp2_fast(t.x - ms);
+          m[g] = mn;
+          l[g] = l[g] * ca[g] + t.y * cb[g];
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float fa = __shfl_sync(0xffffffffu, ca[r / 4], r & 3);
+          const float fb = __shfl_sync(0xffffffffu, cb[r / 4], r & 3);
+#pragma unroll
+          for (int d = 0; d < kDims; d += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(src + r * D + d);
+            o[r][d] = o[r][d] * fa + x.x * fb;
+            o[r][d + 1] = o[r][d + 1] * fa + x.y * fb;
+          }
+        }
+      }
+    }
+    if (warp == 0) {
+      const bool whole = w.whole();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float M = __shfl_sync(0xffffffffu, m[r / 4], r & 3);
+        const float L = __shfl_sync(0xffffffffu, l[r / 4], r & 3);
+        int token, head;
+        if (!row_place(a, w.s, w.qt, w.hm, r, &token, &head)) continue;
+        const int64_t tok = int64_t(w.s.q0) + token, at = int64_t(w.slot()) * R + r;
+        const bool some = L > 0.f || L != L;
+        const float f = !whole ? 1.f : (some ? 1.f / L : 0.f);
+        float* dst = whole ? static_cast<float*>(a.out) + tok * a.o_ts + int64_t(head) * a.o_hs
+                           : a.part_o + at * D;
+#pragma unroll
+        for (int d = 0; d < kDims; d += 2)
+          *reinterpret_cast<float2*>(dst + lane * kDims + d) = make_float2(o[r][d] * f, o[r][d + 1] * f);
+        if (lane == 0) {
+          if (!whole) a.part_ml[at] = make_float2(M, L);
+          else if (a.lse) a.lse[tok * a.Hq + head] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+    }
+    __syncthreads();  // the joined sums are read before the next unit copies its queries there
+  }
+  cp_async_wait<0>();
+}
+
+template <int D, int R>
+static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
+  using C = F32Cfg<D, R>;
+  a.R = R;
+  a.TK = kF32Keys;
+  a.mt = (a.G + R - 1) / R;
+  a.tq = a.cu_q && a.mt == 1 ? R / a.G : 1;
+  a.min_steps = 8;
+  a.extra = 2;
+  size_t smem = sizeof(float) * C::kFloats;
+  static_assert(2 * (sizeof(float) * C::kFloats + 1024 + 64) <= 233472, "two CTAs per SM");
+  if (smem < kPlanScratch) smem = kPlanScratch;
+  auto* k = paged_f32_kernel<D, R>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  const int grid = paged_grid(2);
+  e = launch_kernel(k, dim3(grid), dim3(kF32Threads), smem, s, false, a);
+  if (e != cudaSuccess) return e;
+  return launch_paged_join(a, D, false, grid, s);
+}
+
+cudaError_t launch_paged_f32(const PagedArgs& a, int D, cudaStream_t s) {
+  const bool few = !a.cu_q && a.G <= 4;
+  if (D == 128) return few ? launch_f32<128, 4>(a, s) : launch_f32<128, 16>(a, s);
+  return few ? launch_f32<64, 4>(a, s) : launch_f32<64, 16>(a, s);
+}
+
+}  // namespace fkv

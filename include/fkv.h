@@ -492,7 +492,7 @@ int32_t fkv_step_fp8(const fkv_params_t* p, const fkv_step_io_t* io, const fkv_f
  * attention.  Output rows must not overlap one another or any input, except
  * where an entry point says so.
  * bf16 or fp32 throughout (dtype); D is 64 or 128; page_size is a power of
- * two, 8 .. 1024; at most 8192 sequences, max_pages * page_size <= 2^30, and
+ * two, 8 .. 1024; at most 4096 sequences, max_pages * page_size <= 2^30, and
  * fewer than 2^31 tokens.
  *
  * Device-side errors, recorded as FKV_ERR_DEVICE_ARG in the workspace status

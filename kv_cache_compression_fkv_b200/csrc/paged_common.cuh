@@ -29,8 +29,9 @@
 
 namespace fkv {
 
-constexpr int kMaxPagedSeqs = 8192;  // prefix sums of the division fit in shared memory
-constexpr int kMaxPagedCtas = 296;   // partial slots are sized for two CTAs per SM
+constexpr int kMaxPagedSeqs = 4096;  // prefix sums of the division fit in shared memory
+constexpr int kMaxPagedSms = 148;    // partial slots are sized for this many SMs
+constexpr int kMaxPagedCtas = 4 * kMaxPagedSms;
 
 struct PagedArgs : TileRule {
   const int32_t* page_table;
@@ -279,10 +280,10 @@ struct PagedWs {
   size_t rec, ml, o, total;
 };
 inline PagedWs paged_ws_layout() {
-  // slots x rows is largest for the 128-row tiles with one CTA per SM
-  // (148 * 2 slots * 128 rows); 16-row tiles have 296 * 2 * 16.
+  // two slots per CTA; slots x rows is largest for the 128-row tiles, which have
+  // one CTA per SM (16-row tiles have up to four)
   PagedWs w;
-  const size_t rows = size_t(kMaxPagedCtas) * 128;
+  const size_t rows = size_t(kMaxPagedSms) * 2 * 128;
   w.rec = 256;
   w.ml = w.rec + sizeof(PlanRec) * kMaxPagedCtas;
   w.ml = (w.ml + 255) & ~size_t(255);
@@ -293,8 +294,8 @@ inline PagedWs paged_ws_layout() {
 
 // grid of a kernel with `per_sm` resident CTAs and R rows: every slot fits.
 inline int paged_grid(int per_sm) {
-  const int n = num_sms() * per_sm, most = per_sm * (kMaxPagedCtas / 2);
-  return n < most ? n : most;
+  const int sms = num_sms();
+  return per_sm * (sms < kMaxPagedSms ? sms : kMaxPagedSms);
 }
 
 // Arguments of the norm / rotation / append kernel (paged_rows.cu).

@@ -22,9 +22,9 @@ constexpr int kF32Keys = 32;
 
 template <int D, int R>
 struct F32Cfg {
-  static constexpr int kPitch = D + 16;  // floats per K row: 8 rows x 64 B without conflicts
-  static constexpr int kK = kF32Keys * kPitch, kV = kF32Keys * D;
-  static constexpr int kStages = D == 128 && R == 16 ? 2 : 3;
+  static constexpr int kK = kF32Keys * D, kV = kF32Keys * D;
+  static constexpr int kStages = 2;
+  static constexpr int kPerSm = R == 16 ? 2 : (D == 128 ? 3 : 4);  // resident CTAs
   static constexpr int kQ = R * D;                         // one slot per stage
   static constexpr int kStage = kK + kV + kQ;              // floats
   static constexpr int kOffP = kStages * kStage;           // [32 keys][R]
@@ -32,6 +32,13 @@ struct F32Cfg {
   static constexpr int kOffMl = kOffO + 2 * R * D;         // [2][R] float2
   static constexpr int kFloats = kOffMl + 2 * R * 2;
 };
+
+// Place of 16-byte chunk c of K row r: odd rows swap the halves of each 128
+// bytes, so that the eight lanes of a read (two keys, four chunks) meet no bank twice.
+template <int D>
+__device__ __forceinline__ int k_at(int r, int c) {
+  return r * D + ((c ^ ((r & 1) << 2)) << 2);
+}
 
 __device__ __forceinline__ void cp_async16(float* dst, const void* src, bool read) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -50,43 +57,67 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// The rows that a thread copies of a step: 16 bytes at column `col` of rows
+// row0, row0 + kPass, ...
+template <int D>
+struct Rows {
+  static constexpr int kChunks = D / 4;                 // 16-byte chunks per row
+  static constexpr int kPass = kF32Threads / kChunks;   // rows per pass
+  static constexpr int kCount = kF32Keys / kPass;
+};
+
+// Table entries of the pages that hold this thread's rows of step i of a unit,
+// fetched one step ahead of their use (-1: the row is not wanted).
+template <int D>
+__device__ __forceinline__ void fetch_pages(const PagedArgs& a, const Walk& w, int i,
+                                            int (&ids)[Rows<D>::kCount], unsigned& want) {
+  const int k0 = block_at(w.t, w.first + i) * kF32Keys + int(threadIdx.x) / Rows<D>::kChunks;
+  want = 0;
+#pragma unroll
+  for (int p = 0; p < Rows<D>::kCount; ++p) {
+    const int j = k0 + p * Rows<D>::kPass;
+    const bool read = j < w.s.kv && (j < w.s.pre || (j >= w.t.lo && j <= w.t.hi));
+    ids[p] = -1;
+    if (read) {
+      ids[p] = a.page_table[int64_t(w.b) * a.table_stride + (j >> a.page_shift)];
+      want |= 1u << p;
+    }
+  }
+}
+
 // Starts the copies of step i of a unit into a stage, and of the unit's queries
 // with its first step.
 template <int D, int R>
-__device__ __forceinline__ void load_step(const PagedArgs& a, const Walk& w, int i, float* stage) {
+__device__ __forceinline__ void load_step(const PagedArgs& a, const Walk& w, int i, float* stage,
+                                          const int (&ids)[Rows<D>::kCount], unsigned want) {
   using C = F32Cfg<D, R>;
-  constexpr int kChunks = D / 4;  // 16-byte chunks per row
-  const int h = w.hm / a.mt;
-  const int k0 = block_at(w.t, w.first + i) * kF32Keys;
-  const float* kc = static_cast<const float*>(a.k_cache) + int64_t(h) * a.head_stride;
-  const float* vc = static_cast<const float*>(a.v_cache) + int64_t(h) * a.head_stride;
-  constexpr int kPass = kF32Threads / kChunks;  // rows per pass
-  const int c = (threadIdx.x % kChunks) * 4;
+  constexpr int kChunks = Rows<D>::kChunks, kPass = Rows<D>::kPass;
+  const int row0 = int(threadIdx.x) / kChunks, c = (int(threadIdx.x) % kChunks) * 4;
+  const int k0 = block_at(w.t, w.first + i) * kF32Keys + row0;
+  const int64_t head = int64_t(w.hm / a.mt) * a.head_stride + c;
+  const float* kc = static_cast<const float*>(a.k_cache) + head;
+  const float* vc = static_cast<const float*>(a.v_cache) + head;
+  const float* none = static_cast<const float*>(a.q);  // an address to name when nothing is read
 #pragma unroll
-  for (int p = 0; p < kF32Keys / kPass; ++p) {
-    const int r = p * kPass + threadIdx.x / kChunks, j = k0 + r;
-    bool read = j < w.s.kv && (j < w.s.pre || (j >= w.t.lo && j <= w.t.hi));
-    int64_t off = 0;
-    if (read) {
-      const int id = page_id(a, w.b, j >> a.page_shift);
-      read = id >= 0;
-      if (read)
-        off = int64_t(id) * a.page_stride + int64_t(j & ((1 << a.page_shift) - 1)) * a.row_stride;
-    }
-    const float* none = static_cast<const float*>(a.q);  // an address to name when nothing is read
-    cp_async16(stage + r * C::kPitch + c, read ? kc + off + c : none, read);
-    cp_async16(stage + C::kK + r * D + c, read ? vc + off + c : none, read);
+  for (int p = 0; p < Rows<D>::kCount; ++p) {
+    const int r = row0 + p * kPass, j = k0 + p * kPass, id = ids[p];
+    const bool read = id >= 0 && id < a.num_pages;
+    if (!read && (want >> p & 1u)) report(a.status, FKV_ERR_DEVICE_ARG, w.b);
+    const int64_t off =
+        int64_t(id) * a.page_stride + int64_t(j & ((1 << a.page_shift) - 1)) * a.row_stride;
+    cp_async16(stage + k_at<D>(r, c / 4), read ? kc + off : none, read);
+    cp_async16(stage + C::kK + r * D + c, read ? vc + off : none, read);
   }
   if (i == 0) {
     float* Q = stage + C::kK + C::kV;
 #pragma unroll
     for (int p = 0; p < (R + kPass - 1) / kPass; ++p) {
-      const int r = p * kPass + threadIdx.x / kChunks;
+      const int r = row0 + p * kPass;
       if (r < R) {
-        int token, head;
-        const bool read = row_place(a, w.s, w.qt, w.hm, r, &token, &head);
-        const float* src = static_cast<const float*>(a.q);
-        if (read) src += int64_t(w.s.q0 + token) * a.q_ts + int64_t(head) * a.q_hs + c;
+        int token, head_q;
+        const bool read = row_place(a, w.s, w.qt, w.hm, r, &token, &head_q);
+        const float* src = none;
+        if (read) src += int64_t(w.s.q0 + token) * a.q_ts + int64_t(head_q) * a.q_hs + c;
         cp_async16(Q + r * D + c, src, read);
       }
     }
@@ -94,7 +125,7 @@ __device__ __forceinline__ void load_step(const PagedArgs& a, const Walk& w, int
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_kernel(const PagedArgs a) {
   using C = F32Cfg<D, R>;
   constexpr int kDims = D / 32;  // output dims per lane
   constexpr int kGroups = R / 4;
@@ -114,15 +145,18 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedArgs 
   Walk lw, w;
   lw.begin(a, rec);
   w.begin(a, rec);
-  int li = 0, ln = 0;
+  int li = 0, ln = 0, ids[Rows<D>::kCount];
+  unsigned want = 0;
+  if (!lw.done()) fetch_pages<D>(a, lw, 0, ids, want);
   auto load_next = [&]() {
     if (!lw.done()) {
-      load_step<D, R>(a, lw, li, sm + (ln % C::kStages) * C::kStage);
+      load_step<D, R>(a, lw, li, sm + (ln % C::kStages) * C::kStage, ids, want);
       ++ln;
       if (++li == lw.count) {
         li = 0;
         lw.next(a);
       }
+      if (!lw.done()) fetch_pages<D>(a, lw, li, ids, want);
     }
     cp_async_commit();
   };
@@ -170,7 +204,7 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(const PagedArgs 
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const int d = (4 * c + sub) * 4;
-        const float4 k4 = *reinterpret_cast<const float4*>(stage + key * C::kPitch + d);
+        const float4 k4 = *reinterpret_cast<const float4*>(stage + k_at<D>(key, 4 * c + sub));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float4 q4 = *reinterpret_cast<const float4*>(Q + r * D + d);
@@ -333,12 +367,14 @@ static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
   a.min_steps = 8;
   a.extra = 2;
   size_t smem = sizeof(float) * C::kFloats;
-  static_assert(2 * (sizeof(float) * C::kFloats + 1024 + 64) <= 233472, "two CTAs per SM");
   if (smem < kPlanScratch) smem = kPlanScratch;
+  static_assert(C::kPerSm * (sizeof(float) * C::kFloats + 1024 + 64) <= 233472 &&
+                    C::kPerSm * (kPlanScratch + 1024 + 64) <= 233472,
+                "resident CTAs per SM");
   auto* k = paged_f32_kernel<D, R>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  const int grid = paged_grid(2);
+  const int grid = paged_grid(C::kPerSm);
   e = launch_kernel(k, dim3(grid), dim3(kF32Threads), smem, s, false, a);
   if (e != cudaSuccess) return e;
   return launch_paged_join(a, D, false, grid, s);

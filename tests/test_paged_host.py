@@ -56,7 +56,7 @@ BAD = [
     ({"dtype": 2}, 1), ({"flags": 2}, 1), ({"head_dim": 96}, 3), ({"head_dim": 0}, 2),
     ({"num_q_heads": 7}, 2), ({"num_q_heads": 0}, 2), ({"num_kv_heads": 0}, 2), ({"num_q_heads": 65536}, 2),
     ({"page_size": 12}, 3), ({"page_size": 4}, 3), ({"page_size": 2048}, 3), ({"page_size": 0}, 2),
-    ({"num_pages": -1}, 2), ({"num_seqs": -1}, 2), ({"num_seqs": 8193}, 2), ({"max_pages": -1}, 2),
+    ({"num_pages": -1}, 2), ({"num_seqs": -1}, 2), ({"num_seqs": 4097}, 2), ({"max_pages": -1}, 2),
     ({"max_pages": 1 << 27, "table_stride": 1 << 27}, 2), ({"window": -1}, 2),
     ({"scale": 0.0}, 1), ({"scale": float("nan")}, 1), ({"scale": float("inf")}, 1),
     ({"softcap": -1.0}, 1), ({"softcap": float("nan")}, 1), ({"softcap": float("inf")}, 1),

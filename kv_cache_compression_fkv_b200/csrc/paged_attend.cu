@@ -39,6 +39,9 @@ constexpr int kPaK = 8, kPaV = 10, kPaMma = 9;  // warps: K and Q, V, MMA issuer
 constexpr float kPaRescale = 8.0f;              // P stays <= 2^8 between rescales
 constexpr int kPaPolyEvery = 8;                 // one exponential pair in 8 on the FMA pipe
 
+#ifndef FKV_PA_EXTRA
+#define FKV_PA_EXTRA 6
+#endif
 #ifndef FKV_PA_Q
 #define FKV_PA_Q 2
 #endif
@@ -80,6 +83,11 @@ struct Streams {
   // position in the load and MMA order: s0 b0, s1 b0, s0 b1, s1 b1, ...
   __device__ __forceinline__ int pos(int h, int j) const { return j < nb1 ? 2 * j + h : nb1 + j; }
 };
+
+// The lowest n bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
 
 // One operand of the key blocks, loaded by a whole warp.
 template <int D, int kStages>
@@ -333,10 +341,16 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
             for (int i = 0; i < 128; ++i) sr[i] = __float_as_uint(SV(i) + fmaf(slope, float(i), off));
           }
           if (!full) {
-            const int c_pre = w.s.pre - k0, c_lo = rs.lo - k0, c_hi = rs.hi - k0;
+            // columns that this row sees, one bit each: few instructions per column
+            // keep the code of masked blocks small
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (!(i < c_pre || (i >= c_lo && i <= c_hi))) sr[i] = 0xff800000u;  // -inf
+            for (int c = 0; c < 4; ++c) {
+              const int k = k0 + 32 * c;
+              const uint32_t seen = low_bits(w.s.pre - k) | (low_bits(rs.hi + 1 - k) & ~low_bits(rs.lo - k));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(seen >> i & 1u)) sr[32 * c + i] = 0xff800000u;  // -inf
+            }
           }
           float mx[8];
 #pragma unroll
@@ -494,11 +508,12 @@ template <int D>
 static cudaError_t launch_attend(PagedArgs a, cudaStream_t s) {
   using namespace sm100;
   using C = PaCfg<D>;
-  a.R = a.TK = 128;
+  a.R = 128;
+  a.tk_shift = 7;
   a.mt = (a.G + 127) / 128;
   a.tq = a.mt == 1 ? 128 / a.G : 1;
   a.min_steps = 4;
-  a.extra = 3;
+  a.extra = FKV_PA_EXTRA;
   CUtensorMap tq, tk, tv;
   if (!paged_tmaps(a, D, true, 128, a.mt == 1 ? a.G : 128, a.tq, &tq, &tk, &tv))
     return cudaErrorNotSupported;

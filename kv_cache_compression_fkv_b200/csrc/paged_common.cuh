@@ -68,6 +68,7 @@ struct PlanRec {
   int per;           // length of a part
   int count;         // length of this part (0: none)
   int pad;
+  Seq s;             // the sequence
 };
 
 __device__ __forceinline__ Seq load_seq(const PagedArgs& a, int b) {
@@ -99,53 +100,117 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ Seq seq_of_lane(const Seq& s, int src) {
+  Seq r;
+  r.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+  r.q_len = __shfl_sync(0xffffffffu, s.q_len, src);
+  r.kv = __shfl_sync(0xffffffffu, s.kv, src);
+  r.pre = __shfl_sync(0xffffffffu, s.pre, src);
+  return r;
+}
 
-// Length of one sequence's units (of one KV head), computed by the whole warp.
-__device__ __forceinline__ int64_t seq_length_warp(const PagedArgs& a, int b, int lane) {
-  const Seq s = load_seq(a, b);
+// Length of each lane's sequence (of one head unit); sequences of many query
+// tiles are counted by the whole warp.
+__device__ __forceinline__ int64_t seq_lengths(const PagedArgs& a, const Seq& s, int lane) {
   const int nq = query_tiles(a, s);
+  const bool wide = nq > 8;
   int64_t w = 0;
-  for (int qt = lane; qt < nq; qt += 32) w += tile_span(a, s, qt).n + a.extra;
-  return warp_sum(w);
+  if (!wide)
+    for (int qt = 0; qt < nq; ++qt) w += tile_span(a, s, qt).n + a.extra;
+  unsigned todo = __ballot_sync(0xffffffffu, wide);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const Seq t = seq_of_lane(s, src);
+    const int tiles = query_tiles(a, t);
+    int64_t sum = 0;
+    for (int qt = lane; qt < tiles; qt += 32) sum += tile_span(a, t, qt).n + a.extra;
+    sum = warp_sum(sum);
+    if (lane == src) w = sum;
+  }
+  return w;
+}
+
+// Place `rest` of sequence r.s: query tile, head unit and place in the unit (by
+// the whole warp; r is the same in every lane).
+__device__ __forceinline__ void find_in_seq(const PagedArgs& a, PlanRec& r, int64_t rest, int lane) {
+  const int hm_n = a.Hkv * a.mt, nq = query_tiles(a, r.s);
+  for (int q0 = 0; q0 < nq; q0 += 32) {
+    const int qt = q0 + lane;
+    const int n = qt < nq ? tile_span(a, r.s, qt).n + a.extra : 0;
+    const int64_t len = int64_t(n) * hm_n, inc = warp_scan(len, lane);
+    const unsigned past = __ballot_sync(0xffffffffu, inc > rest);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      const int64_t in = __shfl_sync(0xffffffffu, rest - (inc - len), src);
+      r.n = __shfl_sync(0xffffffffu, n, src);
+      r.qt = q0 + src;
+      r.hm = int(in / r.n);
+      r.j = int(in - int64_t(r.hm) * r.n);
+      return;
+    }
+    rest -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+}
+
+// Part of this CTA of a line of `total`.
+__device__ __forceinline__ PlanRec part_of(const PagedArgs& a, int64_t total, int64_t* start) {
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < a.min_steps) per = a.min_steps;
+  *start = per * blockIdx.x;
+  const int64_t count = total - *start < per ? total - *start : per;
+  PlanRec r = {};
+  r.per = int(per);
+  r.count = count > 0 ? int(count) : 0;
+  return r;
 }
 
 // The division: every thread of the CTA calls it; `scratch` is shared memory
 // (free again afterwards), `rec` the shared result.  Ends with a __syncthreads.
+// Up to 32 sequences are divided by one warp in registers; more by the CTA, with
+// their prefix sums in the scratch.
 constexpr size_t kPlanScratch = sizeof(int64_t) * (32 + kMaxPagedSeqs + 1);
 template <int kThreads>
 __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, PlanRec* rec) {
-  int64_t* warp_tot = scratch;     // [kThreads / 32]
-  int64_t* cum = scratch + 32;     // [B + 1] length of the sequences before b
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hm_n = a.Hkv * a.mt;
+  const Seq none = {0, 0, 0, 0};
+  if (a.B <= 32) {
+    if (warp == 0) {
+      const Seq s = lane < a.B ? load_seq(a, lane) : none;
+      const int64_t w = seq_lengths(a, s, lane) * hm_n, inc = warp_scan(w, lane);
+      int64_t start;
+      PlanRec r = part_of(a, __shfl_sync(0xffffffffu, inc, 31), &start);
+      if (r.count > 0) {
+        const int src = __ffs(__ballot_sync(0xffffffffu, inc > start)) - 1;
+        r.b = src;
+        r.s = seq_of_lane(s, src);
+        find_in_seq(a, r, start - __shfl_sync(0xffffffffu, inc - w, src), lane);
+      }
+      if (lane == 0) {
+        *rec = r;
+        a.rec[blockIdx.x] = r;
+      }
+    }
+    __syncthreads();
+    return;
+  }
+  int64_t* warp_tot = scratch;     // [kThreads / 32]
+  int64_t* cum = scratch + 32;     // [B + 1] length of the sequences before b
   int64_t carry = 0;
   if (tid == 0) cum[0] = 0;
   for (int base = 0; base < a.B; base += kThreads) {
     const int b = base + tid;
-    int64_t w = 0;
-    bool wide = false;
-    if (b < a.B) {
-      const Seq s = load_seq(a, b);
-      const int nq = query_tiles(a, s);
-      wide = nq > 2;
-      if (!wide)
-        for (int qt = 0; qt < nq; ++qt) w += tile_span(a, s, qt).n + a.extra;
-    }
-    // sequences of many query tiles are counted by the warp together
-    unsigned todo = __ballot_sync(0xffffffffu, wide);
-    while (todo) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int64_t t = seq_length_warp(a, base + (warp << 5) + src, lane);
-      if (lane == src) w = t;
-    }
-    w *= hm_n;
-    int64_t inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
+    const Seq s = b < a.B ? load_seq(a, b) : none;
+    const int64_t inc = warp_scan(seq_lengths(a, s, lane) * hm_n, lane);
     if (lane == 31) warp_tot[warp] = inc;
     __syncthreads();
     int64_t before = carry, all = 0;
@@ -159,16 +224,9 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
     __syncthreads();
   }
   if (warp == 0) {
-    const int64_t total = carry;
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < a.min_steps) per = a.min_steps;
-    const int64_t start = per * blockIdx.x;
-    int64_t count = total - start < per ? total - start : per;
-    if (count < 0) count = 0;
-    PlanRec r = {};
-    r.per = int(per);
-    r.count = int(count);
-    if (count > 0) {
+    int64_t start;
+    PlanRec r = part_of(a, carry, &start);
+    if (r.count > 0) {
       int lo = 0, hi = a.B - 1;  // the sequence with cum[b] <= start < cum[b + 1]
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -176,31 +234,8 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
         else lo = mid + 1;
       }
       r.b = lo;
-      const Seq s = load_seq(a, lo);
-      const int nq = query_tiles(a, s);
-      int64_t rest = start - cum[lo];
-      for (int q0 = 0; q0 < nq; q0 += 32) {
-        const int qt = q0 + lane;
-        const int n = qt < nq ? tile_span(a, s, qt).n + a.extra : 0;
-        int64_t inc = int64_t(n) * hm_n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, inc > rest);
-        if (past) {
-          const int src = __ffs(past) - 1;
-          const int64_t in_tile = rest - (inc - int64_t(n) * hm_n);  // lane src: place in its tile
-          const int64_t in = __shfl_sync(0xffffffffu, in_tile, src);
-          r.n = __shfl_sync(0xffffffffu, n, src);
-          r.qt = q0 + src;
-          r.hm = int(in / r.n);
-          r.j = int(in - int64_t(r.hm) * r.n);
-          break;
-        }
-        rest -= __shfl_sync(0xffffffffu, inc, 31);
-      }
+      r.s = load_seq(a, lo);
+      find_in_seq(a, r, start - cum[lo], lane);
     }
     if (lane == 0) {
       *rec = r;
@@ -225,7 +260,7 @@ struct Walk {
     at = r.j;
     left = r.count;
     if (left > 0) {
-      s = load_seq(a, b);
+      s = r.s;
       t = tile_span(a, s, qt);
       cut(a);
       if (count == 0) next(a);

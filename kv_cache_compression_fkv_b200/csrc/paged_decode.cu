@@ -25,7 +25,7 @@ namespace fkv {
 namespace sm100 {
 
 constexpr int kDecThreads = 160;  // four consumer warps, one producer warp
-constexpr int kDecKeys = 64;
+constexpr int kDecKeys = 1 << 6;
 constexpr int kDecRows = 16;
 
 template <int D>
@@ -401,7 +401,7 @@ static cudaError_t launch_decode(PagedArgs a, cudaStream_t s) {
   using namespace sm100;
   using C = DecCfg<D>;
   a.R = kDecRows;
-  a.TK = kDecKeys;
+  a.tk_shift = 6;
   a.mt = (a.G + kDecRows - 1) / kDecRows;
   a.tq = 1;
   a.min_steps = 4;

@@ -18,7 +18,7 @@
 namespace fkv {
 
 constexpr int kF32Threads = 128;
-constexpr int kF32Keys = 32;
+constexpr int kF32Keys = 1 << 5;
 
 template <int D, int R>
 struct F32Cfg {
@@ -361,7 +361,7 @@ template <int D, int R>
 static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
   using C = F32Cfg<D, R>;
   a.R = R;
-  a.TK = kF32Keys;
+  a.tk_shift = 5;
   a.mt = (a.G + R - 1) / R;
   a.tq = a.cu_q && a.mt == 1 ? R / a.G : 1;
   a.min_steps = 8;

@@ -21,7 +21,7 @@ struct Seq {
 
 struct TileRule {
   int G, Hkv;          // query heads per KV head, KV heads
-  int R, TK, tq, mt;   // rows per tile, keys per step, tokens per tile, head slices per KV head
+  int R, tk_shift, tq, mt;  // rows per tile, log2 of keys per step, tokens per tile, head slices
   int window, causal;
 };
 
@@ -41,10 +41,10 @@ FKV_HD Span tile_span(const TileRule& g, const Seq& s, int qt) {
   Span t;
   t.hi = g.causal ? last : s.kv - 1;
   t.lo = g.window > 0 && first - g.window + 1 > 0 ? first - g.window + 1 : 0;
-  t.nA = (s.pre + g.TK - 1) / g.TK;
-  t.from = t.lo / g.TK;
+  t.nA = (s.pre + (1 << g.tk_shift) - 1) >> g.tk_shift;
+  t.from = t.lo >> g.tk_shift;
   if (t.from < t.nA) t.from = t.nA;
-  const int end = t.hi < t.lo ? 0 : t.hi / g.TK + 1;
+  const int end = t.hi < t.lo ? 0 : (t.hi >> g.tk_shift) + 1;
   t.n = t.nA + (end > t.from ? end - t.from : 0);
   if (t.n == 0) t.n = 1;  // rows that see nothing are still written: one masked step
   return t;

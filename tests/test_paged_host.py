@@ -194,7 +194,8 @@ int main() {
     g.G = 1 + rnd(40);
     g.Hkv = 1 + rnd(3);
     g.R = (it & 1) ? 16 : 128;
-    g.TK = (it & 2) ? 64 : 128;
+    g.tk_shift = (it & 2) ? 6 : 7;
+    const int TK = 1 << g.tk_shift;
     g.mt = (g.G + g.R - 1) / g.R;
     g.tq = g.mt == 1 ? g.R / g.G : 1;
     g.causal = rnd(3) > 0;
@@ -228,9 +229,9 @@ int main() {
             const bool want = ((!g.causal || j <= p) && (!g.window || j > p - g.window)) || j < s.pre;
             if (see != want) return 3;
             if (!see) continue;
-            if (visits[j / g.TK] != 1) return 4;
+            if (visits[j / TK] != 1) return 4;
             if (!(j < s.pre || (j >= t.lo && j <= t.hi))) return 5;
-            seen[j / g.TK] = 1;
+            seen[j / TK] = 1;
           }
         }
       for (int blk = 0; blk < 64; ++blk) {

@@ -574,8 +574,10 @@ int32_t fkv_qk_norm_rope(const fkv_rope_t* r, int32_t dtype, int32_t head_dim, i
                          void* stream);
 
 /* Bytes of workspace of the paged entry points (zeroed once with
- * fkv_workspace_init, 256-byte aligned; the status block, then the partial
- * results of work split over the keys).  The same for every fkv_paged_t. */
+ * fkv_workspace_init, 256-byte aligned; the status block, then counters, which
+ * every call leaves zero, and the partial results of work split over the keys).
+ * The same for every fkv_paged_t.  After FKV_ERR_TIMEOUT the workspace has to be
+ * zeroed again. */
 int32_t fkv_paged_workspace_size(size_t* bytes);
 
 /* Appends num_tokens new rows of k and v to the cache at their positions, with

@@ -161,6 +161,7 @@ int32_t check_paged_ws(void* ws, PagedArgs* a) {
   char* base = static_cast<char*>(ws);
   a->status = reinterpret_cast<int32_t*>(base);
   a->rec = reinterpret_cast<PlanRec*>(base + w.rec);
+  a->arrived = reinterpret_cast<int*>(base + w.arrived);
   a->part_ml = reinterpret_cast<float2*>(base + w.ml);
   a->part_o = reinterpret_cast<float*>(base + w.o);
   return FKV_OK;

@@ -14,12 +14,13 @@
 // made on the GPU from cu_q, kv_len and prefix_len, so a captured call stays
 // valid when the lengths change.
 //
-// Join.  A unit whose steps are cut by a part boundary is finished by
-// paged_join_kernel from the partial softmaxes (maximum, sum, unnormalised
-// output, all fp32) of the CTAs that share it.  A CTA leaves at most two: of a
-// unit that began in an earlier part (slot 0), and of the unit that goes on in
-// the next (slot 1).  They are merged in CTA order, so results do not depend on
-// timing.
+// Join.  A unit whose steps are cut by a part boundary is finished from the
+// partial softmaxes (maximum, sum, unnormalised output, all fp32) of the CTAs
+// that share it.  A CTA leaves at most two: of a unit that began in an earlier
+// part (slot 0), and of the unit that goes on in the next (slot 1).  They are
+// merged in CTA order, so results do not depend on timing.  Who merges: the CTA
+// that writes a unit's last partial, where the kernel can and no unit has many;
+// paged_join_kernel otherwise.
 #pragma once
 
 #include <cuda.h>
@@ -44,6 +45,7 @@ struct PagedArgs : TileRule {
   int page_shift, num_pages, max_pages, num_tokens;
   int min_steps;  // smallest part worth a CTA
   int extra;      // what a unit costs besides its steps, in steps
+  int join_here;  // cut units are joined by the kernel itself
   float scale, cap;
   // rows
   const void* q;
@@ -57,6 +59,7 @@ struct PagedArgs : TileRule {
   // workspace
   int32_t* status;
   struct PlanRec* rec;  // [kMaxPagedCtas]
+  int* arrived;         // [kMaxPagedCtas] partials written, per first cut boundary
   float2* part_ml;      // [slot][R] (max in base 2, sum)
   float* part_o;        // [slot][R][D]
 };
@@ -252,8 +255,10 @@ struct Walk {
   int b, qt, hm;
   int at, left;      // place inside the unit, what is left of the part
   int first, count;  // steps of the unit in this part: first .. first + count - 1
+  int64_t from;      // where the unit begins on the line
 
   __device__ __forceinline__ void begin(const PagedArgs& a, const PlanRec& r) {
+    from = int64_t(r.per) * blockIdx.x - r.j;
     b = r.b;
     qt = r.qt;
     hm = r.hm;
@@ -273,6 +278,7 @@ struct Walk {
     do {
       left -= t.n + a.extra - at;
       if (left <= 0) return;
+      from += t.n + a.extra;
       at = 0;
       if (++hm >= a.Hkv * a.mt) {
         hm = 0;
@@ -286,6 +292,13 @@ struct Walk {
       }
       cut(a);
     } while (count == 0);
+  }
+  // The first part boundary that cuts the unit's steps, and the CTAs that share
+  // them.
+  __device__ __forceinline__ int cut_at(const PagedArgs& a, int per, int* parts) const {
+    const int c = int((from + a.extra) / per) + 1;
+    *parts = int((from + t.n + a.extra - 1) / per) - c + 2;
+    return c;
   }
   __device__ __forceinline__ void cut(const PagedArgs& a) {
     const int end = t.n + a.extra - at < left ? t.n + a.extra : at + left;
@@ -311,8 +324,24 @@ __device__ __forceinline__ float tanh_fast(float x) {
   return fmaf(-2.f, r, 1.f);
 }
 
+// Most partials that the last CTA of a unit merges itself.  Measured (131 keys,
+// one sequence of 8 KV heads: no unit cut in two, but that is the GPU's to know): 8.6
+// us a call with the merge inside, 11.7 with a join kernel behind; with 37
+// partials a unit (200k keys) 140 us inside, 133 with the kernel, whose CTAs share
+// the rows.
+constexpr int kJoinHere = 8;
+
+// Whether no unit can be cut into more than kJoinHere parts.  A unit is at most as
+// long as the page table allows, a part at least min_steps; and the units of a
+// sequence are alike, so one has at most 1 / (head units) of the line.
+inline bool few_parts(const PagedArgs& a, int grid) {
+  const int64_t keys = int64_t(a.max_pages) << a.page_shift;
+  const int64_t longest = ((keys + (1 << a.tk_shift) - 1) >> a.tk_shift) + a.extra;
+  return longest / a.min_steps + 2 <= kJoinHere || grid / (a.Hkv * a.mt) + 2 <= kJoinHere;
+}
+
 struct PagedWs {
-  size_t rec, ml, o, total;
+  size_t rec, arrived, ml, o, total;
 };
 inline PagedWs paged_ws_layout() {
   // two slots per CTA; slots x rows is largest for the 128-row tiles, which have
@@ -320,7 +349,8 @@ inline PagedWs paged_ws_layout() {
   PagedWs w;
   const size_t rows = size_t(kMaxPagedSms) * 2 * 128;
   w.rec = 256;
-  w.ml = w.rec + sizeof(PlanRec) * kMaxPagedCtas;
+  w.arrived = w.rec + sizeof(PlanRec) * kMaxPagedCtas;
+  w.ml = w.arrived + sizeof(int) * kMaxPagedCtas;
   w.ml = (w.ml + 255) & ~size_t(255);
   w.o = w.ml + rows * sizeof(float2);
   w.total = w.o + rows * 128 * sizeof(float);

@@ -42,8 +42,11 @@ struct DecCfg {
 struct DecBars {
   uint64_t full[6], empty[6], q_full[2], q_empty[2];
   uint64_t read, wrote;    // merge: every warp has read the last block / written its sums
+  // join: every warp has stored its partial / knows who joins / gathered the sums
+  uint64_t stored, last, gathered;
   float2 ml[4][kDecRows];  // (max, sum) of each warp
   PlanRec rec;
+  int joins;  // this CTA wrote the last partial of the unit
   int abort;
 };
 
@@ -82,6 +85,50 @@ __device__ __forceinline__ bool consumers_meet(uint64_t* bar, uint32_t parity, i
   return warp_wait(bar, parity, abort);
 }
 
+// The last CTA of a unit joins its `parts` (at most kJoinHere) partials, in CTA
+// order: the four consumer warps take four columns of a row per thread.  s_ml:
+// scratch of parts * 16 float2.
+template <int D>
+__device__ __forceinline__ bool join_here(const PagedArgs& a, const Walk& w, int cut, int parts,
+                                          int head0, int rows, float2* s_ml, uint64_t* gathered,
+                                          uint32_t parity, volatile int* abort) {
+  const int tid = threadIdx.x;  // 0 .. 127
+  auto slot_row = [&](int i) {  // first row of partial i
+    return int64_t(i == 0 ? 2 * cut - 1 : 2 * (cut - 1 + i)) * kDecRows;
+  };
+  for (int k = tid; k < parts * kDecRows; k += 128)
+    if ((k & 15) < rows) s_ml[k] = __ldcg(a.part_ml + slot_row(k >> 4) + (k & 15));
+  if (!consumers_meet(gathered, parity, tid & 31, abort)) return false;
+  for (int e = tid * 4; e < rows * D; e += 512) {
+    const int row = e / D, col = e % D;
+    float M = -INFINITY, L = 0.f;
+    for (int i = 0; i < parts; ++i) M = fmaxf(M, s_ml[i * kDecRows + row].x);
+    const float Ms = M == -INFINITY ? 0.f : M;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kJoinHere; ++i) {
+      if (i >= parts) break;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_row(i) + row) * D + col));
+      const float2 ml = s_ml[i * kDecRows + row];
+      const float f = ex2(ml.x - Ms);
+      L = fmaf(ml.y, f, L);
+      y.x = fmaf(v.x, f, y.x);
+      y.y = fmaf(v.y, f, y.y);
+      y.z = fmaf(v.z, f, y.z);
+      y.w = fmaf(v.w, f, y.w);
+    }
+    const bool some = L > 0.f || L != L;
+    const float inv = some ? 1.f / L : 0.f;
+    const int head = head0 + row;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + int64_t(w.s.q0) * a.o_ts +
+                              int64_t(head) * a.o_hs + col) =
+        make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+    if (a.lse && col == 0)
+      a.lse[int64_t(w.s.q0) * a.Hq + head] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  }
+  return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kDecThreads, 2)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -104,14 +151,24 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
     }
     mbar_init(&bars->read, 4);
     mbar_init(&bars->wrote, 4);
+    mbar_init(&bars->stored, 4);
+    mbar_init(&bars->last, 4);
+    mbar_init(&bars->gathered, 4);
     bars->abort = 0;
     fence_mbar_init();
+  }
+  if (threadIdx.x == 128) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
   }
   // the ring is free scratch until the first load; the fence orders that use
   // before the copies of the async proxy
   plan_part<kDecThreads>(a, reinterpret_cast<int64_t*>(sm), &bars->rec);
-  fence_proxy_async_smem();
-  __syncthreads();
+  if (a.B > 32) {
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   Walk w;
   w.begin(a, bars->rec);
   if (warp == 4) {
@@ -172,7 +229,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
     const float kLog2e = 1.4426950408889634f;
     const float sl2 = a.scale * kLog2e;
     const int quad = lane >> 2, col = (lane & 3) * 2;
-    uint32_t n = 0, u = 0;
+    uint32_t n = 0, u = 0, joined = 0, gathers = 0;
     bool ok = true;
     for (; ok && !w.done(); w.next(a), ++u) {
       const int h = w.hm / a.mt, m0 = (w.hm - h * a.mt) * kDecRows;
@@ -361,22 +418,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
           y[c + 7] = fmaf(v1.w, f, y[c + 7]);
         }
       }
-      const int g = m0 + row;
-      if (g < a.G) {
-        const int head = h * a.G + g;
-        if (w.whole()) {
-          const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + int64_t(w.s.q0) * a.o_ts +
-                               int64_t(head) * a.o_hs + part * (D / 8);
-#pragma unroll
-          for (int c = 0; c < D / 8; c += 8)
-            *reinterpret_cast<uint4*>(dst + c) =
-                make_uint4(pack_bf16(y[c] * inv, y[c + 1] * inv), pack_bf16(y[c + 2] * inv, y[c + 3] * inv),
-                           pack_bf16(y[c + 4] * inv, y[c + 5] * inv), pack_bf16(y[c + 6] * inv, y[c + 7] * inv));
-          if (a.lse && part == 0)
-            a.lse[int64_t(w.s.q0) * a.Hq + head] =
-                L > 0.f || L != L ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-        } else {
+      const int g = m0 + row, head = h * a.G + g;
+      if (!w.whole()) {
+        if (g < a.G) {
           const int64_t at = int64_t(w.slot()) * kDecRows + row;
           float* dst = a.part_o + at * D + part * (D / 8);
 #pragma unroll
@@ -384,6 +428,40 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
             *reinterpret_cast<float4*>(dst + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
           if (part == 0) a.part_ml[at] = make_float2(M, L);
         }
+        if (a.join_here) {
+          // the CTA that arrives last joins the partials, in CTA order
+          int parts;
+          const int cut = w.cut_at(a, bars->rec.per, &parts);
+          __threadfence();
+          if (!(ok = consumers_meet(&bars->stored, joined & 1, lane, abort))) break;
+          if (threadIdx.x == 0) {
+            const int before = atomicAdd(&a.arrived[cut], 1);
+            __threadfence();
+            bars->joins = before == parts - 1;
+            if (bars->joins) a.arrived[cut] = 0;  // as the next call finds it
+          }
+          if (!(ok = consumers_meet(&bars->last, joined & 1, lane, abort))) break;
+          ++joined;
+          if (bars->joins) {
+            if (!(ok = join_here<D>(a, w, cut, parts, h * a.G + m0, min(a.G - m0, kDecRows),
+                                    reinterpret_cast<float2*>(xo), &bars->gathered, gathers++ & 1,
+                                    abort)))
+              break;
+          }
+        }
+      }
+      if (w.whole() && g < a.G) {
+        const bool some = L > 0.f || L != L;
+        const float inv = some ? 1.f / L : 0.f;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + int64_t(w.s.q0) * a.o_ts +
+                             int64_t(head) * a.o_hs + part * (D / 8);
+#pragma unroll
+        for (int c = 0; c < D / 8; c += 8)
+          *reinterpret_cast<uint4*>(dst + c) =
+              make_uint4(pack_bf16(y[c] * inv, y[c + 1] * inv), pack_bf16(y[c + 2] * inv, y[c + 3] * inv),
+                         pack_bf16(y[c + 4] * inv, y[c + 5] * inv), pack_bf16(y[c + 6] * inv, y[c + 7] * inv));
+        if (a.lse && part == 0)
+          a.lse[int64_t(w.s.q0) * a.Hq + head] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
       }
       fence_proxy_async_smem();  // the stage was used as scratch: before its next copy
       __syncwarp();
@@ -416,9 +494,10 @@ static cudaError_t launch_decode(PagedArgs a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const int grid = paged_grid(2);
+  a.join_here = few_parts(a, grid);
   e = launch_kernel(k, dim3(grid), dim3(kDecThreads), smem, s, false, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_paged_join(a, D, true, grid, s);
+  return a.join_here ? cudaSuccess : launch_paged_join(a, D, true, grid, s);
 }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int D, cudaStream_t s) {

@@ -23,6 +23,9 @@ DECODE = {
     "g33_d64": Batch(kv=[70], hk=1, g=33, D=64),
     "split": Batch(kv=[5003], hk=1, g=4, page=64),
     "split_many": Batch(kv=[3001, 17, 2500], hk=3, g=2),
+    # short tables: the kernel joins cut units itself (up to 8 parts)
+    "cut_inside": Batch(kv=[900, 1, 850, 77, 1500, 1501], hk=1, g=6, page=32),
+    "cut_inside_d64": Batch(kv=[1500] * 3, hk=3, g=17, D=64),
     "window": Batch(kv=[1, 40, 41, 500, 1500], window=40),
     "window1": Batch(kv=[1, 40, 500], window=1),
     "window_prefix": Batch(kv=[1, 40, 500, 1500, 20], window=40, prefix=[3, 0, 70, 64, 99]),

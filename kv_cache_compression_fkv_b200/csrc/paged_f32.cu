@@ -9,9 +9,8 @@
 // shuffles; for P V a lane owns D / 32 output dims.  Every warp keeps the running
 // maximum, sum and output of the R rows for its keys, so the warps meet once per
 // block (for the ring) and join at the end of a unit.
-// R = 4 for single tokens of up to four query heads per KV head: per 32 KB block
-// (D = 128) about 350 issue slots a scheduler, a quarter of what HBM leaves.  R =
-// 16 otherwise: a chunk packs 16 (token, head) rows, bound by the FMA pipe and
+// R = 1 and 4 for single tokens of one and of up to four query heads per KV head
+// (issue slots per block and row count most there).  R = 16 otherwise: a chunk packs 16 (token, head) rows, bound by the FMA pipe and
 // the broadcast reads of Q (20 shared-memory wavefronts per 64 FMAs of a warp).
 #include "paged_common.cuh"
 
@@ -25,10 +24,11 @@ struct F32Cfg {
   static constexpr int kK = kF32Keys * D, kV = kF32Keys * D;
   static constexpr int kStages = 2;
   static constexpr int kPerSm = R == 16 ? 2 : (D == 128 ? 3 : 4);  // resident CTAs
+  static constexpr int kP = R == 1 ? 4 : R;                // floats per key of P
   static constexpr int kQ = R * D;                         // one slot per stage
   static constexpr int kStage = kK + kV + kQ;              // floats
-  static constexpr int kOffP = kStages * kStage;           // [32 keys][R]
-  static constexpr int kOffO = kOffP + kF32Keys * R;       // [2][R][D]
+  static constexpr int kOffP = kStages * kStage;           // [32 keys][kP]
+  static constexpr int kOffO = kOffP + kF32Keys * kP;      // [2][R][D]
   static constexpr int kOffMl = kOffO + 2 * R * D;         // [2][R] float2
   static constexpr int kFloats = kOffMl + 2 * R * 2;
 };
@@ -71,7 +71,12 @@ struct Rows {
 template <int D>
 __device__ __forceinline__ void fetch_pages(const PagedArgs& a, const Walk& w, int i,
                                             int (&ids)[Rows<D>::kCount], unsigned& want) {
-  const int k0 = block_at(w.t, w.first + i) * kF32Keys + int(threadIdx.x) / Rows<D>::kChunks;
+  const int block = block_at(w.t, w.first + i) * kF32Keys;
+  const int k0 = block + int(threadIdx.x) / Rows<D>::kChunks;
+  const int32_t* table = a.page_table + int64_t(w.b) * a.table_stride;
+  const bool one = (1 << a.page_shift) >= kF32Keys;  // the block lies in one page
+  int id = -1;
+  if (one && block < w.s.kv) id = table[block >> a.page_shift];
   want = 0;
 #pragma unroll
   for (int p = 0; p < Rows<D>::kCount; ++p) {
@@ -79,7 +84,7 @@ __device__ __forceinline__ void fetch_pages(const PagedArgs& a, const Walk& w, i
     const bool read = j < w.s.kv && (j < w.s.pre || (j >= w.t.lo && j <= w.t.hi));
     ids[p] = -1;
     if (read) {
-      ids[p] = a.page_table[int64_t(w.b) * a.table_stride + (j >> a.page_shift)];
+      ids[p] = one ? id : table[j >> a.page_shift];
       want |= 1u << p;
     }
   }
@@ -128,7 +133,7 @@ template <int D, int R>
 __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_kernel(const PagedArgs a) {
   using C = F32Cfg<D, R>;
   constexpr int kDims = D / 32;  // output dims per lane
-  constexpr int kGroups = R / 4;
+  constexpr int kGroups = R == 1 ? 1 : R / 4;
   extern __shared__ __align__(16) float sm[];
   __shared__ PlanRec rec;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
     float slope[kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const int r = 4 * g + sub;
+      const int r = R == 1 ? 0 : 4 * g + sub;
       const int i = a.mt == 1 ? r % a.G : m0 + r;
       pos[g] = p0 + (a.mt == 1 ? r / a.G : 0);
       slope[g] = a.slopes && i < a.G ? a.slopes[h * a.G + i] : 0.f;
@@ -219,14 +224,21 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
       bool grew = false;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        // four dot products over four lanes: lane `sub` ends with row 4 g + sub
-        float u = sub & 1 ? z[4 * g] : z[4 * g + 1], v = sub & 1 ? z[4 * g + 2] : z[4 * g + 3];
-        u = __shfl_xor_sync(0xffffffffu, u, 1);
-        v = __shfl_xor_sync(0xffffffffu, v, 1);
-        const float s01 = (sub & 1 ? z[4 * g + 1] : z[4 * g]) + u;
-        const float s23 = (sub & 1 ? z[4 * g + 3] : z[4 * g + 2]) + v;
-        const float t = __shfl_xor_sync(0xffffffffu, sub & 2 ? s01 : s23, 2);
-        float x = ((sub & 2 ? s23 : s01) + t) * a.scale;
+        float x;
+        if constexpr (R == 1) {
+          x = z[0] + __shfl_xor_sync(0xffffffffu, z[0], 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+        } else {
+          // four dot products over four lanes: lane `sub` ends with row 4 g + sub
+          float u = sub & 1 ? z[4 * g] : z[4 * g + 1], v = sub & 1 ? z[4 * g + 2] : z[4 * g + 3];
+          u = __shfl_xor_sync(0xffffffffu, u, 1);
+          v = __shfl_xor_sync(0xffffffffu, v, 1);
+          const float s01 = (sub & 1 ? z[4 * g + 1] : z[4 * g]) + u;
+          const float s23 = (sub & 1 ? z[4 * g + 3] : z[4 * g + 2]) + v;
+          const float t = __shfl_xor_sync(0xffffffffu, sub & 2 ? s01 : s23, 2);
+          x = (sub & 2 ? s23 : s01) + t;
+        }
+        x *= a.scale;
         if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
         if (a.slopes) x = fmaf(slope[g], float(j - pos[g]), x);
         x *= kLog2e;
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
         const float p = exp2_fast(x - ms);
         l[g] = l[g] * corr[g] + p;
         m[g] = mn;
-        P[key * R + 4 * g + sub] = p;
+        if (R > 1 || sub == 0) P[key * C::kP + (R == 1 ? 0 : 4 * g + sub)] = p;
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -263,9 +275,14 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
         for (int d = 0; d < kDims; d += 2)
           *reinterpret_cast<float2*>(&vv[d]) =
               *reinterpret_cast<const float2*>(V + (warp * 8 + k) * D + d);
+        if constexpr (R == 1) {
+          const float p = P[(warp * 8 + k) * C::kP];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const float4 p = *reinterpret_cast<const float4*>(P + (warp * 8 + k) * R + 4 * g);
+          for (int d = 0; d < kDims; ++d) o[0][d] = fmaf(p, vv[d], o[0][d]);
+        }
+#pragma unroll
+        for (int g = 0; g < R / 4; ++g) {
+          const float4 p = *reinterpret_cast<const float4*>(P + (warp * 8 + k) * C::kP + 4 * g);
 #pragma unroll
           for (int d = 0; d < kDims; ++d) {
             o[4 * g][d] = fmaf(p.x, vv[d], o[4 * g][d]);
@@ -299,7 +316,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
 #pragma unroll
           for (int d = 0; d < kDims; d += 2)
             *reinterpret_cast<float2*>(dst + r * D + d) = make_float2(o[r][d], o[r][d + 1]);
-        if (lane < 4)
+        if (lane < (R == 1 ? 1 : 4))
 #pragma unroll
           for (int g = 0; g < kGroups; ++g)
             ML[(warp - half) * R + 4 * g + lane] = make_float2(m[g], l[g]);
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
         float ca[kGroups], cb[kGroups];
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          const float2 t = ML[warp * R + 4 * g + sub];
+          const float2 t = ML[warp * R + (R == 1 ? 0 : 4 * g + sub)];
           const float mn = fmaxf(m[g], t.x), ms = mn == -INFINITY ? 0.f : mn;
           ca[g] = exp2_fast(m[g] - ms);
           cb[g] = exp2_fast(t.x - ms);
@@ -381,9 +398,10 @@ static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
 }
 
 cudaError_t launch_paged_f32(const PagedArgs& a, int D, cudaStream_t s) {
-  const bool few = !a.cu_q && a.G <= 4;
-  if (D == 128) return few ? launch_f32<128, 4>(a, s) : launch_f32<128, 16>(a, s);
-  return few ? launch_f32<64, 4>(a, s) : launch_f32<64, 16>(a, s);
+  // fewer rows than R cost the products of all R
+  if (!a.cu_q && a.G == 1) return D == 128 ? launch_f32<128, 1>(a, s) : launch_f32<64, 1>(a, s);
+  if (!a.cu_q && a.G <= 4) return D == 128 ? launch_f32<128, 4>(a, s) : launch_f32<64, 4>(a, s);
+  return D == 128 ? launch_f32<128, 16>(a, s) : launch_f32<64, 16>(a, s);
 }
 
 }  // namespace fkv

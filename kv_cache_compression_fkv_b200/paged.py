@@ -24,6 +24,10 @@ import torch
 from . import _lib
 
 _DTYPES = {torch.bfloat16: _lib.FKV_DTYPE_BF16, torch.float32: _lib.FKV_DTYPE_FP32}
+# What torch.cuda.current_stream(index).cuda_stream and torch.cuda.current_device()
+# return, without the objects in between.
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _pack_rows = struct.Struct("=Qqq").pack     # fkv_rows_t
 _pack_batch = struct.Struct("=QQQ").pack    # kv_len, cu_q, prefix_len of fkv_paged_t
 _pack_places = struct.Struct("=Qq").pack    # positions, axis_stride of fkv_rope_t
@@ -32,7 +36,7 @@ _pack_places = struct.Struct("=Qq").pack    # positions, axis_stride of fkv_rope
 def _call(name: str, index: int, stream, *args):
     """One library call on device `index`; its last argument is the stream."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
+        handle = _current_stream(index)
     elif isinstance(stream, torch.cuda.Stream):
         if stream.device_index != index:
             raise ValueError(f"stream is on device {stream.device_index}, the call on device {index}")
@@ -40,7 +44,7 @@ def _call(name: str, index: int, stream, *args):
     else:
         handle = int(stream)
     fn = getattr(_lib.load(), name)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):

@@ -89,6 +89,32 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
+// x <- outer tanh(inner x) of 32 logits, tanh(y) = 1 - 2 / (e^2y + 1).  Four
+// denominators share one reciprocal, r = 1 / (d0 d1 d2 d3): the exponentials and
+// reciprocals are what a capped block waits for.  y is clamped to [-9, 9] (tanh is
+// within 3e-8 of 1 there), so the product stays below (e^18 + 1)^4 < 2e31.
+__device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float inner, float outer) {
+  const float k = inner * 2.885390081777927f, most = 9.f * 2.885390081777927f;  // 2 log2 e
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    float y[4], d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e] = __uint_as_float(x[i + e]) * k;
+      d[e] = ex2(fminf(fmaxf(y[e], -most), most)) + 1.f;  // finite, a NaN's too
+    }
+    const float p01 = d[0] * d[1], p23 = d[2] * d[3];
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(p01 * p23));
+    const float r01 = -2.f * r * p23, r23 = -2.f * r * p01;
+    const float t[4] = {fmaf(r01, d[1], 1.f), fmaf(r01, d[0], 1.f), fmaf(r23, d[3], 1.f),
+                        fmaf(r23, d[2], 1.f)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // a NaN stays one, and with its own column
+      x[i + e] = __float_as_uint(y[e] != y[e] ? y[e] : outer * t[e]);
+  }
+}
+
 // One operand of the key blocks, loaded by a whole warp.
 template <int D, int kStages>
 __device__ __forceinline__ bool load_blocks(const PagedArgs& a, const Walk& w, const CUtensorMap* map,
@@ -296,6 +322,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
     const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_addr + 128u * h, tO = tmem + lane_addr + 256u;
     const float sl2 = a.scale * 1.4426950408889634f;
+    const bool plain = a.cap == 0.f && !a.slopes;
     uint32_t use = 0, base = 0, uc = 0;
     bool ok = true;
     for (; ok && !w.done(); w.next(a), ++uc) {
@@ -324,34 +351,40 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         const bool full = k0 + 127 < w.s.pre || (k0 >= all_lo && k0 + 127 <= all_hi);
         if (live) {
+          if (!plain || !full) {
+            // Cap, distance and mask, 32 columns at a time in a loop and back to
+            // tensor memory: unrolled over all 128 in registers, the first pass
+            // through that code waited 5k to 12k cycles for its instructions.
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[32];
+              tmem_ld32(tS + c * 32, x);
+              tmem_ld_wait();
+              const int k = k0 + 32 * c;
+              if (a.cap > 0.f) cap_logits(x, a.scale / a.cap, a.cap / a.scale);
+              if (a.slopes) {
+                const float off = slope * float(k - pos);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(slope, float(i), off));
+              }
+              if (!full) {  // columns that this row sees, one bit each
+                const uint32_t seen =
+                    low_bits(w.s.pre - k) | (low_bits(rs.hi + 1 - k) & ~low_bits(rs.lo - k));
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(seen >> i & 1u)) x[i] = 0xff800000u;  // -inf
+              }
+              tmem_st32(tS + c * 32, x);
+            }
+            tmem_st_wait();
+          }
           uint32_t sr[128];
 #define SV(i) __uint_as_float(sr[i])
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
           tmem_ld_wait();
-          if (a.cap > 0.f) {
-            const float inner = a.scale / a.cap, outer = a.cap / a.scale;
-#pragma unroll
-            for (int i = 0; i < 128; ++i) sr[i] = __float_as_uint(outer * tanh_fast(SV(i) * inner));
-          }
-          if (a.slopes) {
-            const float off = slope * float(k0 - pos);
-#pragma unroll
-            for (int i = 0; i < 128; ++i) sr[i] = __float_as_uint(SV(i) + fmaf(slope, float(i), off));
-          }
-          if (!full) {
-            // columns that this row sees, one bit each: few instructions per column
-            // keep the code of masked blocks small
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int k = k0 + 32 * c;
-              const uint32_t seen = low_bits(w.s.pre - k) | (low_bits(rs.hi + 1 - k) & ~low_bits(rs.lo - k));
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(seen >> i & 1u)) sr[32 * c + i] = 0xff800000u;  // -inf
-            }
-          }
           float mx[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx[k] = fmaxf(SV(k), SV(k + 8));
@@ -462,7 +495,9 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + tok * a.o_ts +
                              int64_t(head) * a.o_hs + h * (D / 2);
-        float* part = a.part_o + at * D + h * (D / 2);
+        // partials by columns of four, rows side by side: a warp's stores are whole lines
+        float4* part = reinterpret_cast<float4*>(a.part_o) + int64_t(w.slot()) * (128 * D / 4) +
+                       h * (D / 8) * 128 + row;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint32_t r0[32], r1[32];
@@ -484,7 +519,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
           } else if (valid) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(part + c * 32 + k * 4) =
+              part[(c * 8 + k) * 128] =
                   make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
           }
         }
@@ -526,7 +561,7 @@ static cudaError_t launch_attend(PagedArgs a, cudaStream_t s) {
   const int grid = paged_grid(1);
   e = launch_kernel(k, dim3(grid), dim3(kPaThreads), smem, s, false, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_paged_join(a, D, true, grid, s);
+  return launch_paged_join(a, D, true, true, grid, s);
 }
 
 cudaError_t launch_paged_attend(const PagedArgs& a, int D, cudaStream_t s) {

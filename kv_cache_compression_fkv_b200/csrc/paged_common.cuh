@@ -61,7 +61,7 @@ struct PagedArgs : TileRule {
   struct PlanRec* rec;  // [kMaxPagedCtas]
   int* arrived;         // [kMaxPagedCtas] partials written, per first cut boundary
   float2* part_ml;      // [slot][R] (max in base 2, sum)
-  float* part_o;        // [slot][R][D]
+  float* part_o;        // [slot][R][D] unnormalised outputs
 };
 
 // Where a CTA's part of the line begins.
@@ -399,7 +399,10 @@ bool paged_tmaps(const PagedArgs& a, int D, bool bf16, int keys, int q_heads, in
                  CUtensorMap* k, CUtensorMap* v);
 cudaError_t launch_paged_decode(const PagedArgs& a, int D, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedArgs& a, int D, cudaStream_t s);
-cudaError_t launch_paged_join(const PagedArgs& a, int D, bool bf16, int grid, cudaStream_t s);
+// columns: the partial outputs lie as [slot][D / 4][R][4] (the chunk kernel's),
+// else as [slot][R][D].
+cudaError_t launch_paged_join(const PagedArgs& a, int D, bool bf16, bool columns, int grid,
+                              cudaStream_t s);
 cudaError_t launch_paged_f32(const PagedArgs& a, int D, cudaStream_t s);
 
 }  // namespace fkv

@@ -497,7 +497,7 @@ static cudaError_t launch_decode(PagedArgs a, cudaStream_t s) {
   a.join_here = few_parts(a, grid);
   e = launch_kernel(k, dim3(grid), dim3(kDecThreads), smem, s, false, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return a.join_here ? cudaSuccess : launch_paged_join(a, D, true, grid, s);
+  return a.join_here ? cudaSuccess : launch_paged_join(a, D, true, false, grid, s);
 }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int D, cudaStream_t s) {

@@ -394,7 +394,7 @@ static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
   const int grid = paged_grid(C::kPerSm);
   e = launch_kernel(k, dim3(grid), dim3(kF32Threads), smem, s, false, a);
   if (e != cudaSuccess) return e;
-  return launch_paged_join(a, D, false, grid, s);
+  return launch_paged_join(a, D, false, false, grid, s);
 }
 
 cudaError_t launch_paged_f32(const PagedArgs& a, int D, cudaStream_t s) {

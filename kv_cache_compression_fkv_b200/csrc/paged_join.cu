@@ -15,7 +15,7 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinFew = 16;  // partials that one warp takes alone
 
 // A row's running sums: maximum, sum and D / 32 output dims per lane.
-template <int D>
+template <int D, bool kColumns>
 struct RowSum {
   static constexpr int kVec = D / 32;
   float m, l, o[kVec];
@@ -29,10 +29,12 @@ struct RowSum {
                                       int parts, int lane) {
 #pragma unroll 4
     for (int i = first; i < parts; i += step) {
-      const int64_t at = int64_t(i == 0 ? 2 * c - 1 : 2 * (c - 1 + i)) * a.R + row;
-      const float2 ml = a.part_ml[at];
+      const int64_t slot = i == 0 ? 2 * c - 1 : 2 * (c - 1 + i);
+      const float2 ml = a.part_ml[slot * a.R + row];
       float x[kVec];
-      const float* src = a.part_o + at * D + lane * kVec;
+      const int d = lane * kVec;
+      const float* src = a.part_o + slot * a.R * D +
+                         (kColumns ? ((d >> 2) * a.R + row) * 4 + (d & 3) : row * D + d);
 #pragma unroll
       for (int v = 0; v < kVec; v += 2)
         *reinterpret_cast<float2*>(&x[v]) = *reinterpret_cast<const float2*>(src + v);
@@ -46,7 +48,7 @@ struct RowSum {
   }
 };
 
-template <typename T, int D>
+template <typename T, int D, bool kColumns>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a) {
   pdl_wait();
   const int c = int(blockIdx.x) + 1;
@@ -65,7 +67,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   if (parts <= kJoinFew) {
     for (int row = int(blockIdx.y) * kJoinWarps + warp; row < a.R; row += int(gridDim.y) * kJoinWarps) {
       if (!row_place(a, s, qt, hm, row, &token, &head)) continue;
-      RowSum<D> sum;
+      RowSum<D, kColumns> sum;
       sum.add(a, c, row, 0, 1, parts, lane);
       const bool some = sum.l > 0.f || sum.l != sum.l;
       const float f = some ? 1.f / sum.l : 0.f;
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   }
   for (int row = blockIdx.y; row < a.R; row += gridDim.y) {
     if (!row_place(a, s, qt, hm, row, &token, &head)) continue;
-    RowSum<D> sum;
+    RowSum<D, kColumns> sum;
     sum.add(a, c, row, warp, kJoinWarps, parts, lane);
 #pragma unroll
     for (int v = 0; v < kVec; ++v) s_o[warp][lane * kVec + v] = sum.o[v];
@@ -107,11 +109,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   }
 }
 
-cudaError_t launch_paged_join(const PagedArgs& a, int D, bool bf16, int grid, cudaStream_t s) {
+cudaError_t launch_paged_join(const PagedArgs& a, int D, bool bf16, bool columns, int grid,
+                              cudaStream_t s) {
   if (grid < 2) return cudaSuccess;
   const dim3 g(unsigned(grid - 1), 16);
-  auto* k = bf16 ? (D == 128 ? paged_join_kernel<__nv_bfloat16, 128> : paged_join_kernel<__nv_bfloat16, 64>)
-                 : (D == 128 ? paged_join_kernel<float, 128> : paged_join_kernel<float, 64>);
+  using B = __nv_bfloat16;
+  auto* k = paged_join_kernel<float, 128, false>;
+  if (!bf16) k = D == 128 ? k : paged_join_kernel<float, 64, false>;
+  else if (columns) k = D == 128 ? paged_join_kernel<B, 128, true> : paged_join_kernel<B, 64, true>;
+  else k = D == 128 ? paged_join_kernel<B, 128, false> : paged_join_kernel<B, 64, false>;
   return launch_kernel(k, g, dim3(kJoinThreads), 0, s, true, a);
 }
 

@@ -493,7 +493,7 @@ int32_t fkv_step_fp8(const fkv_params_t* p, const fkv_step_io_t* io, const fkv_f
  * where an entry point says so.
  * bf16 or fp32 throughout (dtype); D is 64 or 128; page_size is a power of
  * two, 8 .. 1024; at most 4096 sequences, max_pages * page_size <= 2^30, and
- * fewer than 2^31 tokens.
+ * at most 2^30 tokens.
  *
  * Device-side errors, recorded as FKV_ERR_DEVICE_ARG in the workspace status
  * word with the sequence as detail (nothing is read or written out of range):
@@ -518,8 +518,8 @@ typedef struct fkv_paged {
   int32_t max_pages;    /* entries per sequence of page_table, >= 0              */
   int32_t window;       /* W >= 0; W > 0: a query at position p sees keys
                            j > p - W only (and the prefix)                       */
-  float scale;          /* scale of q.k, finite and > 0                          */
-  float softcap;        /* c >= 0, finite; c > 0: scores c * tanh(scale q.k / c) */
+  float scale;          /* scale of q.k, 1e-12 .. 1e12                           */
+  float softcap;        /* 0, or c in 1e-12 .. 1e12: scores c tanh(scale q.k / c) */
   int64_t page_stride, head_stride, row_stride; /* of the caches, in elements    */
   int64_t table_stride; /* elements between sequences of page_table              */
   void* k_cache;

@@ -16,6 +16,9 @@ int32_t launch_status(cudaError_t e) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Positions, windows and token counts stay below 2^30, so that their sums and
+// differences stay inside 32 bits.
+const int64_t kMaxPositions = int64_t(1) << 30;
 const int64_t kMaxStride = int64_t(1) << 37;  // elements; tensor maps end at 2^40 bytes
 
 // Row strides as the kernels use them: 0 where the dimension has one entry.
@@ -99,15 +102,18 @@ int32_t check_paged(const fkv_paged_t* c, int64_t tokens, PagedArgs* a) {
   if (st != FKV_OK) return st;
   if (c->flags & ~FKV_PAGED_CAUSAL) return FKV_ERR_INVALID_ARG;
   if (c->num_seqs < 0 || c->num_seqs > kMaxPagedSeqs || c->num_pages < 0 || c->max_pages < 0 ||
-      c->num_kv_heads < 1 || c->num_q_heads < 1 || c->window < 0 || tokens < 0)
+      c->num_kv_heads < 1 || c->num_q_heads < 1 || c->window < 0 || tokens < 0 ||
+      tokens > kMaxPositions)
     return FKV_ERR_SHAPE;
   if (c->num_q_heads % c->num_kv_heads != 0 || c->num_q_heads > 65535) return FKV_ERR_SHAPE;
   if (c->page_size < 1) return FKV_ERR_SHAPE;
   if (c->page_size < 8 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0)
     return FKV_ERR_UNSUPPORTED;
-  if (int64_t(c->max_pages) * c->page_size > (int64_t(1) << 30)) return FKV_ERR_SHAPE;
-  if (!(c->scale > 0.f) || c->scale > 3.0e38f) return FKV_ERR_INVALID_ARG;
-  if (!(c->softcap >= 0.f) || c->softcap > 3.0e38f) return FKV_ERR_INVALID_ARG;
+  if (int64_t(c->max_pages) * c->page_size > kMaxPositions) return FKV_ERR_SHAPE;
+  // the kernels form scale / softcap, softcap / scale and slope / scale
+  if (!(c->scale >= 1e-12f && c->scale <= 1e12f)) return FKV_ERR_INVALID_ARG;
+  if (c->softcap != 0.f && !(c->softcap >= 1e-12f && c->softcap <= 1e12f))
+    return FKV_ERR_INVALID_ARG;
   const int elem = c->dtype == FKV_DTYPE_BF16 ? 2 : 4;
   const int64_t strides[] = {c->page_stride, c->head_stride, c->row_stride};
   const int64_t counts[] = {c->num_pages, c->num_kv_heads, c->page_size};
@@ -143,7 +149,7 @@ int32_t check_paged(const fkv_paged_t* c, int64_t tokens, PagedArgs* a) {
   a->num_pages = c->num_pages;
   a->max_pages = c->max_pages;
   a->num_tokens = int(tokens);
-  a->window = c->window;
+  a->window = c->window < kMaxPositions ? c->window : int(kMaxPositions);
   a->causal = (c->flags & FKV_PAGED_CAUSAL) != 0;
   a->scale = c->scale;
   a->cap = c->softcap;
@@ -216,7 +222,7 @@ int32_t fkv_qk_norm_rope(const fkv_rope_t* r, int32_t dtype, int32_t head_dim, i
   if (!r) return FKV_ERR_INVALID_ARG;
   int32_t st = check_type(dtype, head_dim);
   if (st != FKV_OK) return st;
-  if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0 || num_q_heads > 65535 ||
+  if (num_tokens < 0 || num_tokens > kMaxPositions || num_q_heads < 0 || num_kv_heads < 0 || num_q_heads > 65535 ||
       num_kv_heads > 65535)
     return FKV_ERR_SHAPE;
   RowsArgs a = {};

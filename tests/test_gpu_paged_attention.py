@@ -44,6 +44,13 @@ DECODE = {
 }
 
 
+# more sequences than one warp, one CTA and one round of a CTA divide
+for _n, _dtype in ((33, "bf16"), (33, "fp32"), (170, "bf16"), (900, "bf16"), (300, "fp32")):
+    DECODE[f"sequences_{_n}_{_dtype}"] = Batch(kv=[(i * 37) % 90 for i in range(_n)], hk=1, g=2, D=64, page=8,
+                                               dtype=_dtype)
+DECODE["window_beyond_all"] = Batch(kv=[1, 200], window=2 ** 31 - 1)
+
+
 @pytest.mark.parametrize("name", DECODE)
 def test_decode(cuda_device, name):
     case = DECODE[name]
@@ -87,6 +94,14 @@ ATTEND = {
                              dtype="fp32"),
     "fp32_g20_whole": Batch(kv=[70], q=[9], hk=1, g=20, dtype="fp32", causal=False),
 }
+
+
+for _n, _dtype in ((33, "bf16"), (33, "fp32"), (400, "bf16")):
+    ATTEND[f"sequences_{_n}_{_dtype}"] = Batch(kv=[(i * 37) % 90 for i in range(_n)],
+                                               q=[min((i * 37) % 90, (i * 5) % 7) for i in range(_n)], hk=1, g=2,
+                                               D=64, page=8, dtype=_dtype, pad=2)
+ATTEND["window_beyond_all"] = Batch(kv=[3, 200], q=[9, 50], window=2 ** 31 - 1)
+ATTEND["many_tiles"] = Batch(kv=[700, 600], q=[700, 600], hk=1, g=16)  # 88 and 75 query tiles
 
 
 @pytest.mark.parametrize("name", ATTEND)
@@ -238,6 +253,29 @@ def test_results_do_not_depend_on_timing(cuda_device):
         s["out"].fill_(7.0)
         decode(s)
         assert torch.equal(s["out"], first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_keys_and_values_in_one_buffer(cuda_device, dtype):
+    """[pages][heads][rows][2][D]: rows of the cache 2 D apart."""
+    case = Batch(kv=[90, 33], q=[20, 33], dtype=dtype)
+    s = case.make()
+    both = torch.stack([s["k_cache"], s["v_cache"]], dim=3)
+    k, v = both[..., 0, :], both[..., 1, :]
+    s["cache"] = fkv.PagedCache(k, v, s["table"], num_q_heads=case.hq)
+    attend(s)
+    check(case, s)
+    assert status(s)[0] == 0
+
+
+def test_pages_shared_by_sequences(cuda_device):
+    """A common prefix in the same pages."""
+    case = Batch(kv=[70, 80, 64], q=[6, 16, 1], nan=False)
+    s = case.make()
+    s["table"][1, :4] = s["table"][0, :4]
+    s["table"][2, :4] = s["table"][0, :4]
+    attend(s)
+    check(case, s)
 
 
 def test_no_tokens_or_sequences(cuda_device):

@@ -170,6 +170,19 @@ def test_append(cuda_device, name, style):
                 close(f64(s2["k_cache"][p[0], :, p[1]]), ref_k[i], mag[i], case.dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_append_turns_queries_in_place(cuda_device, dtype):
+    case = Batch(kv=[40, 50, 60], q=[10, 20, 30], dtype=dtype, nan=False)
+    a, b = case.make(), case.make()
+    rows = torch.randn((60, case.hq + 2 * case.hk, 128), device="cuda").to(DT[dtype])
+    q, k, v = rows.split([case.hq, case.hk, case.hk], dim=1)
+    rope = fkv.make_rope(omega_of(64).cuda(), style="half")
+    out = torch.empty((60, case.hq, 128), dtype=DT[dtype], device="cuda")
+    _append(case, a, rope, k, v, q, out)
+    _append(case, b, rope, k, v, q, q)
+    assert torch.equal(q, out) and torch.equal(a["k_cache"], b["k_cache"])
+
+
 def test_append_one_token_per_sequence_without_offsets(cuda_device):
     case = Batch(kv=[1, 16, 17, 200], q=[1, 1, 1, 1], nan=False)
     a, b = case.make(), case.make()

@@ -59,6 +59,7 @@ BAD = [
     ({"num_pages": -1}, 2), ({"num_seqs": -1}, 2), ({"num_seqs": 4097}, 2), ({"max_pages": -1}, 2),
     ({"max_pages": 1 << 27, "table_stride": 1 << 27}, 2), ({"window": -1}, 2),
     ({"scale": 0.0}, 1), ({"scale": float("nan")}, 1), ({"scale": float("inf")}, 1),
+    ({"scale": 1e-13}, 1), ({"scale": -1.0}, 1), ({"softcap": 1e-13}, 1), ({"softcap": 1e13}, 1),
     ({"softcap": -1.0}, 1), ({"softcap": float("nan")}, 1), ({"softcap": float("inf")}, 1),
     ({"page_stride": 64}, 2), ({"row_stride": 0}, 2), ({"head_stride": -128}, 2), ({"row_stride": 132}, 1),
     ({"row_stride": 1 << 41}, 2), ({"table_stride": 3}, 2),
@@ -97,7 +98,10 @@ def test_bad_rows_and_workspaces_are_refused(lib):
     assert lib.fkv_paged_decode(None, ok, ok, None, FAKE, None) == 1
     assert lib.fkv_paged_decode(c, None, ok, None, FAKE, None) == 1
     assert lib.fkv_paged_decode(c, ok, ok, FAKE + 2, FAKE, None) == 1
-    assert lib.fkv_paged_attend(c, -1, ok, ok, None, FAKE, None) == 2
+    for n in (-1, (1 << 30) + 1):
+        assert lib.fkv_paged_attend(c, n, ok, ok, None, FAKE, None) == 2
+        assert lib.fkv_paged_append(c, None, n, None, ok, ok, None, FAKE, None) == 2
+        assert lib.fkv_qk_norm_rope(_rope(), 0, 128, n, 8, 8, ok, ok, ok, ok, None) == 2
     assert lib.fkv_paged_attend(_paged(cu_q=None), 5, ok, ok, None, FAKE, None) == 2  # 3 sequences
     assert lib.fkv_paged_append(_paged(cu_q=None), None, 5, None, ok, ok, None, FAKE, None) == 2
     assert lib.fkv_paged_append(c, None, 5, ok, ok, ok, None, FAKE, None) == 1  # q without q_out

@@ -176,15 +176,14 @@ struct RowTurn {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a, int runs, int run_rows) {
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a, int run_rows) {
   using R = RowTurn<T, D>;
   constexpr int kVec = R::kVec, kStep = R::kStep, kTpr = R::kTpr;
   __shared__ float2 s_cs[kRowThreads / 32][D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t job = int64_t(blockIdx.x) * (kRowThreads / 32) + warp;
-  const int t = int(job / runs);
+  const int t = int(blockIdx.x) * (kRowThreads / 32) + warp;
   if (t >= a.tokens) return;
-  const int first = int(job - int64_t(t) * runs) * run_rows, end = first + run_rows;
+  const int first = int(blockIdx.y) * run_rows, end = first + run_rows;
   const int i = lane % kTpr;
   const int half_chunks = a.half ? a.pairs / kVec : 0;
   R turn;
@@ -282,11 +281,8 @@ static cudaError_t launch_rows_of(const RowsArgs& a, cudaStream_t s) {
   int run_rows = int((n_rows + runs - 1) / runs);
   run_rows = (run_rows + kStep - 1) / kStep * kStep;
   runs = (n_rows + run_rows - 1) / run_rows;
-  const int64_t jobs = int64_t(a.tokens) * runs;
-  const int64_t ctas = (jobs + kWarps - 1) / kWarps;
-  if (ctas > int64_t(0x7fffffff)) return cudaErrorInvalidConfiguration;
-  return launch_kernel(rows_kernel<T, D>, dim3(unsigned(ctas)), dim3(kRowThreads), 0, s, false, a,
-                       int(runs), run_rows);
+  const dim3 grid(unsigned((a.tokens + kWarps - 1) / kWarps), unsigned(runs));
+  return launch_kernel(rows_kernel<T, D>, grid, dim3(kRowThreads), 0, s, false, a, run_rows);
 }
 
 cudaError_t launch_rows(const RowsArgs& a, bool bf16, int D, cudaStream_t s) {

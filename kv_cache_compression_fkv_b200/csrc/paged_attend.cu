@@ -39,20 +39,19 @@ constexpr int kPaK = 8, kPaV = 10, kPaMma = 9;  // warps: K and Q, V, MMA issuer
 constexpr float kPaRescale = 8.0f;              // P stays <= 2^8 between rescales
 constexpr int kPaPolyEvery = 8;                 // one exponential pair in 8 on the FMA pipe
 
-constexpr int kQStages = 2;  // the next unit's logits start under the last one's merge
 template <int D>
 struct PaCfg {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kTile = 128 * D * 2;
   static constexpr int kKStages = D == 128 ? 3 : 6;
-  static constexpr int kVStages = D == 128 ? 2 : 6;
-  static constexpr uint32_t kOffK = kQStages * kTile;
+  static constexpr int kVStages = D == 128 ? 3 : 6;
+  static constexpr uint32_t kOffK = kTile;
   static constexpr uint32_t kOffV = kOffK + kKStages * kTile;
   static constexpr uint32_t kOffBar = kOffV + kVStages * kTile;
 };
 
 struct PaBars {
-  uint64_t q_full[kQStages], q_empty[kQStages];
+  uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t s_full[2], p_full[2];
   uint64_t o_ready, o_free, mma_done, x_full, x_read;
@@ -168,10 +167,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kQStages; ++s) {
-      mbar_init(&bars->q_full[s], 1);
-      mbar_init(&bars->q_empty[s], 1);
-    }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < kKS; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
@@ -212,22 +209,20 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
       const uint32_t q_bytes = uint32_t(a.mt == 1 ? a.tq * a.G : 128) * 128 * C::kHalves;
       uint32_t n = 0, u = 0;
       for (; !w.done(); w.next(a)) {
-        const uint32_t qs = u % kQStages;
-        if (!warp_wait(&bars->q_empty[qs], ((u / kQStages) & 1) ^ 1, abort)) break;
+        if (!warp_wait(&bars->q_empty, (u & 1) ^ 1, abort)) break;
         if (lane == 0) {
           const int h = w.hm / a.mt, m = w.hm - h * a.mt;
-          mbar_expect_tx(&bars->q_full[qs], q_bytes);
+          mbar_expect_tx(&bars->q_full, q_bytes);
           for (int half = 0; half < C::kHalves; ++half)
-            tma_load_3d(sm + qs * C::kTile + half * kRegionBytes, &tm_q, &bars->q_full[qs],
-                        half * 64, h * a.G + m * 128, w.s.q0 + w.qt * a.tq);
+            tma_load_3d(sm + half * kRegionBytes, &tm_q, &bars->q_full, half * 64,
+                        h * a.G + m * 128, w.s.q0 + w.qt * a.tq);
         }
         ++u;
         if (!load_blocks<D, kKS>(a, w, &tm_k, sm + C::kOffK, bars->k_full, bars->k_empty, n, abort)) break;
       }
       for (uint32_t i = n > kKS ? n - kKS : 0; i < n; ++i)
         drain_wait(&bars->k_full[i % kKS], (i / kKS) & 1);
-      for (uint32_t i = u > kQStages ? u - kQStages : 0; i < u; ++i)
-        drain_wait(&bars->q_full[i % kQStages], (i / kQStages) & 1);
+      if (u > 0) drain_wait(&bars->q_full, (u - 1) & 1);
     } else if (warp == kPaV) {
       // ---------------------------------------------------------- V
       uint32_t n = 0;
@@ -242,46 +237,49 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
       constexpr uint32_t kStageDesc = C::kTile >> 4;
       uint32_t uc = 0, ks = 0, kph = 0, vs = 0, vph = 0;
       uint32_t p_use[2] = {0, 0};
-      bool ok = true;
-      const uint64_t dq0 = kmajor_desc(smem_u32(sm), 0);
+      bool ok = true, kf_ok = false, vf_ok = false;
+      const uint64_t dq = kmajor_desc(smem_u32(sm), 0);
       const uint64_t dk0 = kmajor_desc(smem_u32(sm + C::kOffK), 0);
       const uint64_t dv0 = mnmajor_desc(smem_u32(sm + C::kOffV), 0);
       for (; ok && !w.done(); w.next(a), ++uc) {
         const Streams st(w.count);
         bool o_free_seen = false;
-        uint64_t dq = 0;
+        // O_h += P_h V for the stream's next block.  K and V stages are used in load
+        // order, so the stage of the group that follows is known: its barrier is
+        // tested inside this group's MMAs (kf_ok / vf_ok, as in attend_sm100.cu) and
+        // waited on only when the test saw it pending.
         auto issue_pv = [&](int h, bool first) -> bool {
           if (!o_free_seen) {
             if (!mbar_wait(&bars->o_free, (uc & 1) ^ 1, abort)) return false;
             o_free_seen = true;
           }
-          if (!mbar_wait(&bars->v_full[vs], vph, abort)) return false;
+          if (!vf_ok && !mbar_wait(&bars->v_full[vs], vph, abort)) return false;
+          vf_ok = false;
           if (!mbar_wait(&bars->p_full[h], p_use[h] & 1, abort)) return false;
           ++p_use[h];
           tc_fence_after();
-          const uint64_t dv = dv0 + uint64_t(vs * kStageDesc);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)  // 16 keys: 8 columns of P, 2048 B of V
-            mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + k * 8, dv + uint64_t(k) * 128u, kIdPV,
-                   (first && k == 0) ? 0u : 1u);
+          kf_ok = mma8_ts_probe(tmem + 256u + 128u * h, tmem + 128u * h, dv0 + uint64_t(vs * kStageDesc),
+                                kIdPV, first ? 0u : 1u, &bars->k_full[ks], kph) != 0;
           if (++vs == kVS) { vs = 0; vph ^= 1; }
           return true;
         };
+        // S_h = Q K^T for the stream's next block.
         auto issue_s = [&](int h) -> bool {
-          if (!mbar_wait(&bars->k_full[ks], kph, abort)) return false;
+          if (!kf_ok && !mbar_wait(&bars->k_full[ks], kph, abort)) return false;
+          kf_ok = false;
           const uint64_t dk = dk0 + uint64_t(ks * kStageDesc);
+          if constexpr (D == 128) {
+            vf_ok = mma8_ss_probe(tmem + 128u * h, dq, dk, kIdQK, 0u, &bars->v_full[vs], vph) != 0;
+          } else {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = uint64_t((k >> 2) * (kRegionBytes >> 4) + (k & 3) * 2);
-            mma_ss(tmem + 128u * h, dq + off, dk + off, kIdQK, k > 0 ? 1u : 0u);
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tmem + 128u * h, dq + uint64_t(k * 2), dk + uint64_t(k * 2), kIdQK, k > 0 ? 1u : 0u);
           }
           mma_commit(&bars->s_full[h]);
           if (++ks == kKS) { ks = 0; kph ^= 1; }
           return true;
         };
-        const uint32_t qs = uc % kQStages;
-        dq = dq0 + uint64_t(qs * kStageDesc);
-        if (!(ok = mbar_wait(&bars->q_full[qs], (uc / kQStages) & 1, abort))) break;
+        if (!(ok = mbar_wait(&bars->q_full, uc & 1, abort))) break;
         for (int j = 0; ok && j < st.nb0; ++j) {
           if (j > 0 && !(ok = issue_pv(0, j == 1))) break;
           if (!(ok = issue_s(0))) break;
@@ -293,7 +291,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
         }
         if (!ok) break;
-        mma_commit(&bars->q_empty[qs]);
+        mma_commit(&bars->q_empty);
         if (!(ok = issue_pv(0, st.nb0 == 1))) break;
         if (st.nb1 == st.nb0 && st.nb1 > 0 && !(ok = issue_pv(1, st.nb1 == 1))) break;
         mma_commit(&bars->o_ready);

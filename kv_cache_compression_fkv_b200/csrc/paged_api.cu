@@ -197,9 +197,10 @@ int32_t attention(const fkv_paged_t* c, int64_t tokens, bool single, const fkv_r
   a.o_ts = so.ts;
   a.o_hs = so.hs;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (c->dtype == FKV_DTYPE_FP32) return launch_status(launch_paged_f32(a, c->head_dim, s));
-  if (single) return launch_status(launch_paged_decode(a, c->head_dim, s));
-  return launch_status(launch_paged_attend(a, c->head_dim, s));
+  const bool f32 = c->dtype == FKV_DTYPE_FP32;
+  auto* launch = single ? (f32 ? launch_paged_decode_f32 : launch_paged_decode)
+                        : (f32 ? launch_paged_attend_f32 : launch_paged_attend);
+  return launch_status(launch(a, c->head_dim, s));
 }
 
 }  // namespace

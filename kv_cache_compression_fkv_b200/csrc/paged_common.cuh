@@ -403,6 +403,7 @@ cudaError_t launch_paged_attend(const PagedArgs& a, int D, cudaStream_t s);
 // else as [slot][R][D].
 cudaError_t launch_paged_join(const PagedArgs& a, int D, bool bf16, bool columns, int grid,
                               cudaStream_t s);
-cudaError_t launch_paged_f32(const PagedArgs& a, int D, cudaStream_t s);
+cudaError_t launch_paged_decode_f32(const PagedArgs& a, int D, cudaStream_t s);
+cudaError_t launch_paged_attend_f32(const PagedArgs& a, int D, cudaStream_t s);
 
 }  // namespace fkv

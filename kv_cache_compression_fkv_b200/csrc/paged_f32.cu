@@ -1,5 +1,5 @@
-// Paged attention in fp32 (the library's accuracy mode) on the CUDA cores, one
-// kernel for single tokens and for chunks: fp32 products and sums throughout.
+// Attention of one new token per sequence over the paged cache in fp32 (the
+// library's accuracy mode), on the CUDA cores: fp32 products and sums throughout.
 //
 // The four warps of a CTA stream 32-key blocks of K and V through a ring filled
 // with 16-byte asynchronous copies (rows that no query sees, or of a bad page, are
@@ -9,15 +9,13 @@
 // shuffles; for P V a lane owns D / 32 output dims.  Every warp keeps the running
 // maximum, sum and output of the R rows for its keys, so the warps meet once per
 // block (for the ring) and join at the end of a unit.
-// R = 1 and 4 for single tokens of one and of up to four query heads per KV head
-// (issue slots per block and row count most there).  R = 16 otherwise: a chunk packs 16 (token, head) rows, bound by the FMA pipe and
-// the broadcast reads of Q (20 shared-memory wavefronts per 64 FMAs of a warp).
-#include "paged_common.cuh"
+// Bound by the instructions beside the loads: R = 1, 4 and 16 for up to as many
+// query heads per KV head, since rows that are not there cost as much as others
+// (16 sequences, windows of 1024 keys, one head per KV head: 42 us with R = 1, 51
+// with R = 4; the bytes take 21).
+#include "paged_f32.cuh"
 
 namespace fkv {
-
-constexpr int kF32Threads = 128;
-constexpr int kF32Keys = 1 << 5;
 
 template <int D, int R>
 struct F32Cfg {
@@ -40,89 +38,26 @@ __device__ __forceinline__ int k_at(int r, int c) {
   return r * D + ((c ^ ((r & 1) << 2)) << 2);
 }
 
-__device__ __forceinline__ void cp_async16(float* dst, const void* src, bool read) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src), "r"(read ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The rows that a thread copies of a step: 16 bytes at column `col` of rows
-// row0, row0 + kPass, ...
-template <int D>
-struct Rows {
-  static constexpr int kChunks = D / 4;                 // 16-byte chunks per row
-  static constexpr int kPass = kF32Threads / kChunks;   // rows per pass
-  static constexpr int kCount = kF32Keys / kPass;
-};
-
-// Table entries of the pages that hold this thread's rows of step i of a unit,
-// fetched one step ahead of their use (-1: the row is not wanted).
-template <int D>
-__device__ __forceinline__ void fetch_pages(const PagedArgs& a, const Walk& w, int i,
-                                            int (&ids)[Rows<D>::kCount], unsigned& want) {
-  const int block = block_at(w.t, w.first + i) * kF32Keys;
-  const int k0 = block + int(threadIdx.x) / Rows<D>::kChunks;
-  const int32_t* table = a.page_table + int64_t(w.b) * a.table_stride;
-  const bool one = (1 << a.page_shift) >= kF32Keys;  // the block lies in one page
-  int id = -1;
-  if (one && block < w.s.kv) id = table[block >> a.page_shift];
-  want = 0;
-#pragma unroll
-  for (int p = 0; p < Rows<D>::kCount; ++p) {
-    const int j = k0 + p * Rows<D>::kPass;
-    const bool read = j < w.s.kv && (j < w.s.pre || (j >= w.t.lo && j <= w.t.hi));
-    ids[p] = -1;
-    if (read) {
-      ids[p] = one ? id : table[j >> a.page_shift];
-      want |= 1u << p;
-    }
-  }
-}
-
 // Starts the copies of step i of a unit into a stage, and of the unit's queries
 // with its first step.
 template <int D, int R>
 __device__ __forceinline__ void load_step(const PagedArgs& a, const Walk& w, int i, float* stage,
                                           const int (&ids)[Rows<D>::kCount], unsigned want) {
   using C = F32Cfg<D, R>;
-  constexpr int kChunks = Rows<D>::kChunks, kPass = Rows<D>::kPass;
-  const int row0 = int(threadIdx.x) / kChunks, c = (int(threadIdx.x) % kChunks) * 4;
-  const int k0 = block_at(w.t, w.first + i) * kF32Keys + row0;
-  const int64_t head = int64_t(w.hm / a.mt) * a.head_stride + c;
-  const float* kc = static_cast<const float*>(a.k_cache) + head;
-  const float* vc = static_cast<const float*>(a.v_cache) + head;
-  const float* none = static_cast<const float*>(a.q);  // an address to name when nothing is read
-#pragma unroll
-  for (int p = 0; p < Rows<D>::kCount; ++p) {
-    const int r = row0 + p * kPass, j = k0 + p * kPass, id = ids[p];
-    const bool read = id >= 0 && id < a.num_pages;
-    if (!read && (want >> p & 1u)) report(a.status, FKV_ERR_DEVICE_ARG, w.b);
-    const int64_t off =
-        int64_t(id) * a.page_stride + int64_t(j & ((1 << a.page_shift) - 1)) * a.row_stride;
-    cp_async16(stage + k_at<D>(r, c / 4), read ? kc + off : none, read);
-    cp_async16(stage + C::kK + r * D + c, read ? vc + off : none, read);
-  }
+  load_keys<D>(a, w, i, ids, want, [&](int r, int c) { return stage + k_at<D>(r, c); },
+               [&](int r, int c) { return stage + C::kK + r * D + c * 4; });
   if (i == 0) {
+    constexpr int kPass = Rows<D>::kPass;
+    const int row0 = int(threadIdx.x) / Rows<D>::kChunks, c = int(threadIdx.x) % Rows<D>::kChunks * 4;
     float* Q = stage + C::kK + C::kV;
 #pragma unroll
     for (int p = 0; p < (R + kPass - 1) / kPass; ++p) {
       const int r = row0 + p * kPass;
       if (r < R) {
-        int token, head_q;
-        const bool read = row_place(a, w.s, w.qt, w.hm, r, &token, &head_q);
-        const float* src = none;
-        if (read) src += int64_t(w.s.q0 + token) * a.q_ts + int64_t(head_q) * a.q_hs + c;
+        int token, head;
+        const bool read = row_place(a, w.s, w.qt, w.hm, r, &token, &head);
+        const float* src = static_cast<const float*>(a.q);
+        if (read) src += int64_t(w.s.q0 + token) * a.q_ts + int64_t(head) * a.q_hs + c;
         cp_async16(Q + r * D + c, src, read);
       }
     }
@@ -180,8 +115,8 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int r = R == 1 ? 0 : 4 * g + sub;
-      const int i = a.mt == 1 ? r % a.G : m0 + r;
-      pos[g] = p0 + (a.mt == 1 ? r / a.G : 0);
+      const int i = m0 + r;
+      pos[g] = p0;
       slope[g] = a.slopes && i < a.G ? a.slopes[h * a.G + i] : 0.f;
     }
     float m[kGroups], l[kGroups], o[R][kDims];
@@ -380,7 +315,7 @@ static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
   a.R = R;
   a.tk_shift = 5;
   a.mt = (a.G + R - 1) / R;
-  a.tq = a.cu_q && a.mt == 1 ? R / a.G : 1;
+  a.tq = 1;
   a.min_steps = 8;
   a.extra = 2;
   size_t smem = sizeof(float) * C::kFloats;
@@ -397,10 +332,9 @@ static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
   return launch_paged_join(a, D, false, false, grid, s);
 }
 
-cudaError_t launch_paged_f32(const PagedArgs& a, int D, cudaStream_t s) {
-  // fewer rows than R cost the products of all R
-  if (!a.cu_q && a.G == 1) return D == 128 ? launch_f32<128, 1>(a, s) : launch_f32<64, 1>(a, s);
-  if (!a.cu_q && a.G <= 4) return D == 128 ? launch_f32<128, 4>(a, s) : launch_f32<64, 4>(a, s);
+cudaError_t launch_paged_decode_f32(const PagedArgs& a, int D, cudaStream_t s) {
+  if (a.G == 1) return D == 128 ? launch_f32<128, 1>(a, s) : launch_f32<64, 1>(a, s);
+  if (a.G <= 4) return D == 128 ? launch_f32<128, 4>(a, s) : launch_f32<64, 4>(a, s);
   return D == 128 ? launch_f32<128, 16>(a, s) : launch_f32<64, 16>(a, s);
 }
 

@@ -363,6 +363,23 @@ inline int paged_grid(int per_sm) {
   return per_sm * (sms < kMaxPagedSms ? sms : kMaxPagedSms);
 }
 
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
 // Arguments of the norm / rotation / append kernel (paged_rows.cu).
 struct RowsArgs {
   int tokens, nq, nk, nv;  // heads per token (nv: value rows, append only)

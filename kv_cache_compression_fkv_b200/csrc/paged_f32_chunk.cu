@@ -4,7 +4,7 @@
 // Bound by the FMA pipe.  A CTA takes 64 (token, head) rows, each of its four warps
 // 16 of them against whole 32-key blocks of K and V, which arrive by asynchronous
 // copies one step ahead.  Scores: a lane owns 4 rows x 4 keys (rows 4 rg .., keys
-// kg + 8 i), so 4 + 4 reads of 16 bytes feed 64 FMAs; the blocks are swizzled so
+// kg + 8 i), so 4 + 4 reads of 16 bytes feed 64 FMAs (32 packed ones); the blocks are swizzled so
 // that each read is one wavefront (8 keys side by side, or 4 rows broadcast).
 // P V: 4 rows x D / 8 dims per lane, 1 + D / 32 reads per key for D / 2 FMAs, the
 // probabilities passing through the warp's own corner of shared memory.  A warp
@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
       live |= valid;
     }
     live = __any_sync(0xffffffffu, live);
-    float m[4], l[4], o[4][kCols][4];
+    float m[4], l[4];
+    float2 o[4][kCols][2];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       m[r] = -INFINITY;
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[r][c][e] = 0.f;
+        for (int e = 0; e < 2; ++e) o[r][c][e] = make_float2(0.f, 0.f);
     }
     for (int i = 0; i < w.count; ++i, ++n) {
       cp_async_wait<0>();
@@ -114,11 +115,11 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
       const float* K = sm + (n & 1) * C::kStage;
       const float* V = K + kF32Keys * D;
       const int k0 = block_at(w.t, w.first + i) * kF32Keys;
-      float z[4][4];
+      float2 zz[4][4];  // sums over even and odd dims
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) z[r][k] = 0.f;
+        for (int k = 0; k < 4; ++k) zz[r][k] = make_float2(0.f, 0.f);
 #pragma unroll 2
       for (int c = 0; c < D / 4; ++c) {
         float4 q4[4], k4[4];
@@ -132,13 +133,12 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
         for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            z[r][k] = fmaf(q4[r].x, k4[k].x, z[r][k]);
-            z[r][k] = fmaf(q4[r].y, k4[k].y, z[r][k]);
-            z[r][k] = fmaf(q4[r].z, k4[k].z, z[r][k]);
-            z[r][k] = fmaf(q4[r].w, k4[k].w, z[r][k]);
+            zz[r][k] = fma2(make_float2(q4[r].x, q4[r].y), make_float2(k4[k].x, k4[k].y), zz[r][k]);
+            zz[r][k] = fma2(make_float2(q4[r].z, q4[r].w), make_float2(k4[k].z, k4[k].w), zz[r][k]);
           }
       }
       const bool full = k0 + 31 < w.s.pre || (k0 >= all_lo && k0 + 31 <= all_hi);
+      float z[4][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const RowSpan rs = row_span(a, w.s, pos[r]);
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int j = k0 + kg + 8 * k;
-          float x = z[r][k] * a.scale;
+          float x = (zz[r][k].x + zz[r][k].y) * a.scale;
           if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
           if (a.slopes) x = fmaf(slope[r], float(j - pos[r]), x);
           x *= kLog2e;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[r][c][e] *= corr;
+            for (int e = 0; e < 2; ++e) o[r][c][e] = mul2(o[r][c][e], make_float2(corr, corr));
           m[r] = mn;
         }
       }
@@ -185,22 +185,13 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           const float4 v = *reinterpret_cast<const float4*>(V + k * D + c * 32 + kg * 4);
-          o[0][c][0] = fmaf(p.x, v.x, o[0][c][0]);
-          o[0][c][1] = fmaf(p.x, v.y, o[0][c][1]);
-          o[0][c][2] = fmaf(p.x, v.z, o[0][c][2]);
-          o[0][c][3] = fmaf(p.x, v.w, o[0][c][3]);
-          o[1][c][0] = fmaf(p.y, v.x, o[1][c][0]);
-          o[1][c][1] = fmaf(p.y, v.y, o[1][c][1]);
-          o[1][c][2] = fmaf(p.y, v.z, o[1][c][2]);
-          o[1][c][3] = fmaf(p.y, v.w, o[1][c][3]);
-          o[2][c][0] = fmaf(p.z, v.x, o[2][c][0]);
-          o[2][c][1] = fmaf(p.z, v.y, o[2][c][1]);
-          o[2][c][2] = fmaf(p.z, v.z, o[2][c][2]);
-          o[2][c][3] = fmaf(p.z, v.w, o[2][c][3]);
-          o[3][c][0] = fmaf(p.w, v.x, o[3][c][0]);
-          o[3][c][1] = fmaf(p.w, v.y, o[3][c][1]);
-          o[3][c][2] = fmaf(p.w, v.z, o[3][c][2]);
-          o[3][c][3] = fmaf(p.w, v.w, o[3][c][3]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float2 pr = r == 0 ? make_float2(p.x, p.x) : r == 1 ? make_float2(p.y, p.y)
+                            : r == 2 ? make_float2(p.z, p.z) : make_float2(p.w, p.w);
+            o[r][c][0] = fma2(pr, make_float2(v.x, v.y), o[r][c][0]);
+            o[r][c][1] = fma2(pr, make_float2(v.z, v.w), o[r][c][1]);
+          }
         }
       }
     }
@@ -222,7 +213,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
         *reinterpret_cast<float4*>(dst + c * 32 + kg * 4) =
-            make_float4(o[r][c][0] * f, o[r][c][1] * f, o[r][c][2] * f, o[r][c][3] * f);
+            make_float4(o[r][c][0].x * f, o[r][c][0].y * f, o[r][c][1].x * f, o[r][c][1].y * f);
       if (kg == 0) {
         if (!whole) a.part_ml[at] = make_float2(m[r], L);
         else if (a.lse) a.lse[tok * a.Hq + head] = some ? (m[r] + log2f(L)) * 0.6931471805599453f : -INFINITY;

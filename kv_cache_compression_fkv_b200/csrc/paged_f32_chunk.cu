@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
   constexpr int kCols = D / 32;  // 16-byte columns of the output per lane
   extern __shared__ __align__(16) float sm[];
   __shared__ PlanRec rec;
+  __shared__ int2 place[kChunkRows];  // token and head of a row of the unit; head -1: no row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rg = lane & 3, kg = lane >> 2;  // row group; key group, or dim group
   plan_part<kF32Threads>(a, reinterpret_cast<int64_t*>(sm), &rec);
@@ -74,13 +75,20 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
   int n = 0;
   if (!w.done()) load_next();
   for (; !w.done(); w.next(a)) {
-    __syncthreads();  // the last unit's queries are done with
+    __syncthreads();  // the last unit's queries and places are done with
+    if (threadIdx.x < kChunkRows) {
+      int token, head;
+      const bool valid = row_place(a, w.s, w.qt, w.hm, threadIdx.x, &token, &head);
+      place[threadIdx.x] = make_int2(w.s.q0 + token, valid ? head : -1);
+    }
+    __syncthreads();
+#pragma unroll 2
     for (int e = threadIdx.x; e < kChunkRows * (D / 4); e += kF32Threads) {
       const int r = e / (D / 4), c = e % (D / 4);
-      int token, head;
-      const bool read = row_place(a, w.s, w.qt, w.hm, r, &token, &head);
+      const int2 at = place[r];
+      const bool read = at.y >= 0;
       const float* src = static_cast<const float*>(a.q);
-      if (read) src += int64_t(w.s.q0 + token) * a.q_ts + int64_t(head) * a.q_hs + c * 4;
+      if (read) src += int64_t(at.x) * a.q_ts + int64_t(at.y) * a.q_hs + c * 4;
       cp_async16(Q + q_swz<D>(r, c), src, read);
     }
     cp_async_commit();
@@ -92,10 +100,10 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
     float slope[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      int token, head;
-      const bool valid = row_place(a, w.s, w.qt, w.hm, warp * kWarpRows + rg * 4 + r, &token, &head);
-      pos[r] = w.s.kv - w.s.q_len + token;
-      slope[r] = a.slopes && valid ? a.slopes[head] : 0.f;
+      const int2 at = place[warp * kWarpRows + rg * 4 + r];
+      const bool valid = at.y >= 0;
+      pos[r] = w.s.kv - w.s.q_len + at.x - w.s.q0;
+      slope[r] = a.slopes && valid ? a.slopes[at.y] : 0.f;
       live |= valid;
     }
     live = __any_sync(0xffffffffu, live);
@@ -141,21 +149,42 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
           }
       }
       const bool full = k0 + 31 < w.s.pre || (k0 >= all_lo && k0 + 31 <= all_hi);
+      // options by the block, so that the code of those a call lacks is never fetched
       float z[4][4];
 #pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[r][k] = (zz[r][k].x + zz[r][k].y) * a.scale;
+      if (a.cap > 0.f) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[r][k] = a.cap * tanhf(z[r][k] / a.cap);
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[r][k] = fmaf(slope[r], float(k0 + kg + 8 * k - pos[r]), z[r][k]);
+      }
+      if (!full) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const RowSpan rs = row_span(a, w.s, pos[r]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = k0 + kg + 8 * k;
+            if (!(j < w.s.kv && (j < w.s.pre || (j >= rs.lo && j <= rs.hi)))) z[r][k] = -INFINITY;
+          }
+        }
+      }
+#pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const RowSpan rs = row_span(a, w.s, pos[r]);
         float mx = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int j = k0 + kg + 8 * k;
-          float x = (zz[r][k].x + zz[r][k].y) * a.scale;
-          if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
-          if (a.slopes) x = fmaf(slope[r], float(j - pos[r]), x);
-          x *= kLog2e;
-          if (!full && !(j < w.s.kv && (j < w.s.pre || (j >= rs.lo && j <= rs.hi)))) x = -INFINITY;
-          z[r][k] = x;
-          mx = fmaxf(mx, x);
+          z[r][k] *= kLog2e;
+          mx = fmaxf(mx, z[r][k]);
         }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -199,27 +228,42 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
       }
     }
     if (!live) continue;
+    // the rows leave through the warp's own queries, which are done with: a rolled
+    // loop of whole rows (straight-line code for every row took longer to fetch
+    // than to run)
     const bool whole = w.whole();
+    __syncwarp();
+    float* O = Q + warp * kWarpRows * D;
+    float2* ml = reinterpret_cast<float2*>(P);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      float L = l[r];
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-      const int row = warp * kWarpRows + rg * 4 + r;
-      int token, head;
-      if (!row_place(a, w.s, w.qt, w.hm, row, &token, &head)) continue;
-      const int64_t tok = int64_t(w.s.q0) + token, at = int64_t(w.slot()) * kChunkRows + row;
-      const bool some = L > 0.f || L != L;
-      const float f = !whole ? 1.f : (some ? 1.f / L : 0.f);
-      float* dst = whole ? static_cast<float*>(a.out) + tok * a.o_ts + int64_t(head) * a.o_hs
-                         : a.part_o + at * D;
+      for (int off = 4; off < 32; off <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
-        *reinterpret_cast<float4*>(dst + c * 32 + kg * 4) =
-            make_float4(o[r][c][0].x * f, o[r][c][0].y * f, o[r][c][1].x * f, o[r][c][1].y * f);
-      if (kg == 0) {
-        if (!whole) a.part_ml[at] = make_float2(m[r], L);
-        else if (a.lse) a.lse[tok * a.Hq + head] = some ? (m[r] + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        *reinterpret_cast<float4*>(O + (rg * 4 + r) * D + (c * 8 + (kg ^ rg)) * 4) =
+            make_float4(o[r][c][0].x, o[r][c][0].y, o[r][c][1].x, o[r][c][1].y);
+      if (kg == 0) ml[rg * 4 + r] = make_float2(m[r], l[r]);
+    }
+    __syncwarp();
+    constexpr int kChunks = D / 4;
+#pragma unroll 1
+    for (int e = lane; e < kWarpRows * kChunks; e += 32) {
+      const int r = e / kChunks, c = e % kChunks, row = warp * kWarpRows + r;
+      const int2 to = place[row];
+      if (to.y < 0) continue;
+      const float2 v = ml[r];
+      const bool some = v.y > 0.f || v.y != v.y;
+      const float f = !whole ? 1.f : (some ? 1.f / v.y : 0.f);
+      const int64_t at = int64_t(w.slot()) * kChunkRows + row;
+      float* dst = whole ? static_cast<float*>(a.out) + int64_t(to.x) * a.o_ts + int64_t(to.y) * a.o_hs
+                         : a.part_o + at * D;
+      const float4 x = *reinterpret_cast<const float4*>(O + r * D + (c ^ (r >> 2)) * 4);
+      *reinterpret_cast<float4*>(dst + c * 4) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+      if (c == 0) {
+        if (!whole) a.part_ml[at] = v;
+        else if (a.lse)
+          a.lse[int64_t(to.x) * a.Hq + to.y] = some ? (v.x + log2f(v.y)) * 0.6931471805599453f : -INFINITY;
       }
     }
   }
@@ -236,8 +280,8 @@ static cudaError_t launch_chunk(PagedArgs a, cudaStream_t s) {
   a.min_steps = 8;
   a.extra = 2;
   size_t smem = sizeof(float) * C::kFloats;
-  static_assert(2 * (sizeof(float) * C::kFloats + 1024 + 64) <= 233472 &&
-                    2 * (kPlanScratch + 1024 + 64) <= 233472,
+  static_assert(2 * (sizeof(float) * C::kFloats + 1024 + 1024) <= 233472 &&
+                    2 * (kPlanScratch + 1024 + 1024) <= 233472,
                 "two CTAs per SM");
   if (smem < kPlanScratch) smem = kPlanScratch;
   auto* k = paged_f32_chunk_kernel<D>;

@@ -32,7 +32,8 @@ struct F32Cfg {
   static constexpr int kOffP = kStages * kStage;           // [32 keys][kP]
   static constexpr int kOffO = kOffP + kF32Keys * kP;      // [2][R][D]
   static constexpr int kOffMl = kOffO + 2 * R * D;         // [4][R] float2
-  static constexpr int kFloats = kOffMl + 4 * R * 2;
+  static constexpr int kOffRow = kOffMl + 4 * R * 2;       // [R] (factor, head)
+  static constexpr int kFloats = kOffRow + 2 * (R == 1 ? 2 : R);
 };
 
 // Place of 16-byte chunk c of K row r: odd rows swap the halves of each 128
@@ -81,6 +82,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
   float* P = sm + C::kOffP;
   float* O = sm + C::kOffO;
   float2* ML = reinterpret_cast<float2*>(sm + C::kOffMl);
+  float2* Row = reinterpret_cast<float2*>(sm + C::kOffRow);
   // this lane's key inside a block, and its dims quarter (scores) or row in each
   // group of four (softmax)
   const int key = warp * 8 + (lane >> 2), sub = lane & 3;
@@ -281,30 +283,37 @@ __global__ void __launch_bounds__(kF32Threads, F32Cfg<D, R>::kPerSm) paged_f32_k
       __syncthreads();
     }
     const bool whole = w.whole();
+    if (threadIdx.x < R) {
+      const int r = threadIdx.x;
+      int token, head;
+      if (row_place(a, w.s, w.qt, w.hm, r, &token, &head)) {
+        const int64_t tok = int64_t(w.s.q0) + token;
+        float M = ML[r].x, L = 0.f;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) M = fmaxf(M, ML[i * R + r].x);
+        const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) L = fmaf(ML[i * R + r].y, exp2_fast(ML[i * R + r].x - Ms), L);
+        const bool some = L > 0.f || L != L;
+        if (!whole) a.part_ml[int64_t(w.slot()) * R + r] = make_float2(M, L);
+        else if (a.lse) a.lse[tok * a.Hq + head] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        Row[r] = make_float2(!whole ? 1.f : (some ? 1.f / L : 0.f), __int_as_float(head));
+      } else {
+        Row[r].y = __int_as_float(-1);
+      }
+    }
+    __syncthreads();
 #pragma unroll 1
     for (int e = threadIdx.x; e < R * (D / 4); e += kF32Threads) {
-      const int r = e / (D / 4), d = e % (D / 4) * 4;
-      int token, head;
-      if (!row_place(a, w.s, w.qt, w.hm, r, &token, &head)) continue;
-      float M = ML[r].x, L = 0.f;
-#pragma unroll
-      for (int i = 1; i < 4; ++i) M = fmaxf(M, ML[i * R + r].x);
-      const float Ms = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) L = fmaf(ML[i * R + r].y, exp2_fast(ML[i * R + r].x - Ms), L);
-      const int64_t tok = int64_t(w.s.q0) + token, at = int64_t(w.slot()) * R + r;
-      const bool some = L > 0.f || L != L;
-      const float fr = !whole ? 1.f : (some ? 1.f / L : 0.f);
+      const int r = e / (D / 4), d = e % (D / 4) * 4, head = __float_as_int(Row[r].y);
+      const float fr = Row[r].x;
       const float4 x = *reinterpret_cast<const float4*>(O + r * D + d);
       const float4 y = *reinterpret_cast<const float4*>(O + R * D + r * D + d);
-      float* dst = whole ? static_cast<float*>(a.out) + tok * a.o_ts + int64_t(head) * a.o_hs
-                         : a.part_o + at * D;
-      *reinterpret_cast<float4*>(dst + d) =
-          make_float4((x.x + y.x) * fr, (x.y + y.y) * fr, (x.z + y.z) * fr, (x.w + y.w) * fr);
-      if (d == 0) {
-        if (!whole) a.part_ml[at] = make_float2(M, L);
-        else if (a.lse) a.lse[tok * a.Hq + head] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-      }
+      float* dst = whole ? static_cast<float*>(a.out) + int64_t(w.s.q0) * a.o_ts + int64_t(head) * a.o_hs
+                         : a.part_o + (int64_t(w.slot()) * R + r) * D;
+      if (head >= 0)
+        *reinterpret_cast<float4*>(dst + d) =
+            make_float4((x.x + y.x) * fr, (x.y + y.y) * fr, (x.z + y.z) * fr, (x.w + y.w) * fr);
     }
     __syncthreads();  // the joined sums are read before the next unit copies its queries there
   }
@@ -318,7 +327,7 @@ static cudaError_t launch_f32(PagedArgs a, cudaStream_t s) {
   a.tk_shift = 5;
   a.mt = (a.G + R - 1) / R;
   a.tq = 1;
-  a.min_steps = 8;
+  a.min_steps = 3;
   a.extra = 2;
   size_t smem = sizeof(float) * C::kFloats;
   if (smem < kPlanScratch) smem = kPlanScratch;

@@ -246,25 +246,30 @@ __global__ void __launch_bounds__(kF32Threads, 2) paged_f32_chunk_kernel(const P
       if (kg == 0) ml[rg * 4 + r] = make_float2(m[r], l[r]);
     }
     __syncwarp();
-    constexpr int kChunks = D / 4;
-#pragma unroll 1
-    for (int e = lane; e < kWarpRows * kChunks; e += 32) {
-      const int r = e / kChunks, c = e % kChunks, row = warp * kWarpRows + r;
+    if (lane < kWarpRows) {
+      const int row = warp * kWarpRows + lane;
       const int2 to = place[row];
-      if (to.y < 0) continue;
-      const float2 v = ml[r];
+      const float2 v = ml[lane];
       const bool some = v.y > 0.f || v.y != v.y;
-      const float f = !whole ? 1.f : (some ? 1.f / v.y : 0.f);
-      const int64_t at = int64_t(w.slot()) * kChunkRows + row;
-      float* dst = whole ? static_cast<float*>(a.out) + int64_t(to.x) * a.o_ts + int64_t(to.y) * a.o_hs
-                         : a.part_o + at * D;
-      const float4 x = *reinterpret_cast<const float4*>(O + r * D + (c ^ (r >> 2)) * 4);
-      *reinterpret_cast<float4*>(dst + c * 4) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-      if (c == 0) {
-        if (!whole) a.part_ml[at] = v;
+      if (to.y >= 0) {
+        if (!whole) a.part_ml[int64_t(w.slot()) * kChunkRows + row] = v;
         else if (a.lse)
           a.lse[int64_t(to.x) * a.Hq + to.y] = some ? (v.x + log2f(v.y)) * 0.6931471805599453f : -INFINITY;
       }
+      ml[lane].x = !whole ? 1.f : (some ? 1.f / v.y : 0.f);
+    }
+    __syncwarp();
+    constexpr int kChunks = D / 4;
+#pragma unroll 2
+    for (int e = lane; e < kWarpRows * kChunks; e += 32) {
+      const int r = e / kChunks, c = e % kChunks, row = warp * kWarpRows + r;
+      const int2 to = place[row];
+      const float f = ml[r].x;
+      const float4 x = *reinterpret_cast<const float4*>(O + r * D + (c ^ (r >> 2)) * 4);
+      float* dst = whole ? static_cast<float*>(a.out) + int64_t(to.x) * a.o_ts + int64_t(to.y) * a.o_hs
+                         : a.part_o + (int64_t(w.slot()) * kChunkRows + row) * D;
+      if (to.y >= 0)
+        *reinterpret_cast<float4*>(dst + c * 4) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
     }
   }
   cp_async_wait<0>();
@@ -277,7 +282,7 @@ static cudaError_t launch_chunk(PagedArgs a, cudaStream_t s) {
   a.tk_shift = 5;
   a.mt = (a.G + kChunkRows - 1) / kChunkRows;
   a.tq = a.mt == 1 ? kChunkRows / a.G : 1;
-  a.min_steps = 8;
+  a.min_steps = 3;
   a.extra = 2;
   size_t smem = sizeof(float) * C::kFloats;
   static_assert(2 * (sizeof(float) * C::kFloats + 1024 + 1024) <= 233472 &&

@@ -537,10 +537,17 @@ static cudaError_t launch_attend(PagedArgs a, cudaStream_t s) {
   a.tk_shift = 7;
   a.mt = (a.G + 127) / 128;
   a.tq = a.mt == 1 ? 128 / a.G : 1;
+  // Of parts of the line from 4, 8, 16 blocks up: 31, 33 and 46 us for the 30 mixed
+  // pieces of a batch.
   a.min_steps = 4;
   // What a unit costs besides its blocks, in blocks: the causal prompts of a batch
   // (short units in the first parts) took 866 / 807 / 760 / 755 us at 4 / 5 / 6 / 8.
   a.extra = 6;
+  // Units cut by themselves (own_steps 1 / 2 / 3 / 4): 128 queries over 900 keys, 16
+  // heads: 26.0 / 22.6 / 21.5 / 24.0 us (on the line 22.4); the mixed pieces 28.2,
+  // with slack 3 as slow as on the line.
+  a.own_steps = 3;
+  a.slack = 6;
   CUtensorMap tq, tk, tv;
   if (!paged_tmaps(a, D, true, 128, a.mt == 1 ? a.G : 128, a.tq, &tq, &tk, &tv))
     return cudaErrorNotSupported;
@@ -551,6 +558,7 @@ static cudaError_t launch_attend(PagedArgs a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const int grid = paged_grid(1);
+  a.own_units = grid / (a.Hkv * a.mt);
   e = launch_kernel(k, dim3(grid), dim3(kPaThreads), smem, s, false, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
   return launch_paged_join(a, D, true, true, grid, s);

@@ -14,6 +14,11 @@
 // made on the GPU from cu_q, kv_len and prefix_len, so a captured call stays
 // valid when the lengths change.
 //
+// With no more units than CTAs the cuts go elsewhere when that makes the longest
+// part little longer: every unit into equal parts of its own, one per CTA, so that
+// no CTA has a piece of two units (which is two passes through the code before and
+// behind the steps, most of the time of a short call).
+//
 // Join.  A unit whose steps are cut by a part boundary is finished from the
 // partial softmaxes (maximum, sum, unnormalised output, all fp32) of the CTAs
 // that share it.  A CTA leaves at most two: of a unit that began in an earlier
@@ -34,6 +39,12 @@ constexpr int kMaxPagedSeqs = 4096;  // prefix sums of the division fit in share
 constexpr int kMaxPagedSms = 148;    // partial slots are sized for this many SMs
 constexpr int kMaxPagedCtas = 4 * kMaxPagedSms;
 
+// Most partials that the last CTA of a unit merges itself.  Measured (decode, 8 KV
+// heads, one sequence): 131 keys, no unit cut, but that is the GPU's to know: 8.6 us
+// a call with the merge inside, 11.7 with a join kernel behind; 1000 keys, units cut
+// in 6: 14.3 inside, 13.2 with the kernel; 200k keys, in 37: 140 and 133.
+constexpr int kJoinHere = 4;
+
 struct PagedArgs : TileRule {
   const int32_t* page_table;
   const int32_t* kv_len;
@@ -45,6 +56,9 @@ struct PagedArgs : TileRule {
   int page_shift, num_pages, max_pages, num_tokens;
   int min_steps;  // smallest part worth a CTA
   int extra;      // what a unit costs besides its steps, in steps
+  int own_steps;  // smallest part of a unit that is cut by itself
+  int own_units;  // most units per head for that: CTAs / (Hkv mt)
+  int slack;      // steps that such parts may be longer than those of the line
   int join_here;  // cut units are joined by the kernel itself
   float scale, cap;
   // rows
@@ -70,7 +84,7 @@ struct PlanRec {
   int n;             // length of that unit
   int per;           // length of a part
   int count;         // length of this part (0: none)
-  int pad;
+  int extra;         // of the units in it (0: units are cut by themselves)
   Seq s;             // the sequence
 };
 
@@ -103,10 +117,11 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {  // inclusive
+template <class T>
+__device__ __forceinline__ T warp_scan(T v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
@@ -120,14 +135,20 @@ __device__ __forceinline__ Seq seq_of_lane(const Seq& s, int src) {
   return r;
 }
 
-// Length of each lane's sequence (of one head unit); sequences of many query
-// tiles are counted by the whole warp.
-__device__ __forceinline__ int64_t seq_lengths(const PagedArgs& a, const Seq& s, int lane) {
+// Steps of each lane's sequence (of one head unit), or its parts of up to P > 1
+// steps; *longest: of its units.  Sequences of many query tiles are counted by the
+// whole warp.
+__device__ __forceinline__ int64_t seq_steps(const PagedArgs& a, const Seq& s, int lane, int P, int* longest) {
   const int nq = query_tiles(a, s);
   const bool wide = nq > 8;
   int64_t w = 0;
+  *longest = 0;
   if (!wide)
-    for (int qt = 0; qt < nq; ++qt) w += tile_span(a, s, qt).n + a.extra;
+    for (int qt = 0; qt < nq; ++qt) {
+      const int n = parts_of(tile_span(a, s, qt).n, P);
+      w += n;
+      if (n > *longest) *longest = n;
+    }
   unsigned todo = __ballot_sync(0xffffffffu, wide);
   while (todo) {
     const int src = __ffs(todo) - 1;
@@ -135,44 +156,65 @@ __device__ __forceinline__ int64_t seq_lengths(const PagedArgs& a, const Seq& s,
     const Seq t = seq_of_lane(s, src);
     const int tiles = query_tiles(a, t);
     int64_t sum = 0;
-    for (int qt = lane; qt < tiles; qt += 32) sum += tile_span(a, t, qt).n + a.extra;
+    int most = 0;
+    for (int qt = lane; qt < tiles; qt += 32) {
+      const int n = parts_of(tile_span(a, t, qt).n, P);
+      sum += n;
+      if (n > most) most = n;
+    }
     sum = warp_sum(sum);
-    if (lane == src) w = sum;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == src) {
+      w = sum;
+      *longest = most;
+    }
   }
   return w;
 }
 
 // Place `rest` of sequence r.s: query tile, head unit and place in the unit (by
-// the whole warp; r is the same in every lane).
-__device__ __forceinline__ void find_in_seq(const PagedArgs& a, PlanRec& r, int64_t rest, int lane) {
+// the whole warp; r is the same in every lane).  P = 0: the place on the line;
+// else the number of a part of up to P steps.
+__device__ __forceinline__ void find_in_seq(const PagedArgs& a, PlanRec& r, int64_t rest, int P, int lane) {
   const int hm_n = a.Hkv * a.mt, nq = query_tiles(a, r.s);
   for (int q0 = 0; q0 < nq; q0 += 32) {
     const int qt = q0 + lane;
-    const int n = qt < nq ? tile_span(a, r.s, qt).n + a.extra : 0;
-    const int64_t len = int64_t(n) * hm_n, inc = warp_scan(len, lane);
+    const int n = qt < nq ? tile_span(a, r.s, qt).n + r.extra : 0;
+    const int u = P ? parts_of(n, P) : n;
+    const int64_t len = int64_t(u) * hm_n, inc = warp_scan(len, lane);
     const unsigned past = __ballot_sync(0xffffffffu, inc > rest);
     if (past) {
       const int src = __ffs(past) - 1;
       const int64_t in = __shfl_sync(0xffffffffu, rest - (inc - len), src);
+      const int of = __shfl_sync(0xffffffffu, u, src);
       r.n = __shfl_sync(0xffffffffu, n, src);
       r.qt = q0 + src;
-      r.hm = int(in / r.n);
-      r.j = int(in - int64_t(r.hm) * r.n);
+      r.hm = int(in / of);
+      r.j = int(in - int64_t(r.hm) * of);
+      if (P) {
+        r.j *= P;
+        r.per = P;
+        r.count = r.n - r.j < P ? r.n - r.j : P;
+      }
       return;
     }
     rest -= __shfl_sync(0xffffffffu, inc, 31);
   }
 }
 
-// Part of this CTA of a line of `total`.
-__device__ __forceinline__ PlanRec part_of(const PagedArgs& a, int64_t total, int64_t* start) {
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < a.min_steps) per = a.min_steps;
+// Length of a part of a line of `total`.
+__device__ __forceinline__ int64_t line_part(const PagedArgs& a, int64_t total) {
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  return per < a.min_steps ? a.min_steps : per;
+}
+// Part of this CTA of the line.
+__device__ __forceinline__ PlanRec part_of(const PagedArgs& a, int64_t total, int64_t per, int64_t* start) {
   *start = per * blockIdx.x;
   const int64_t count = total - *start < per ? total - *start : per;
   PlanRec r = {};
   r.per = int(per);
   r.count = count > 0 ? int(count) : 0;
+  r.extra = a.extra;
   return r;
 }
 
@@ -189,14 +231,33 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
   if (a.B <= 32) {
     if (warp == 0) {
       const Seq s = lane < a.B ? load_seq(a, lane) : none;
-      const int64_t w = seq_lengths(a, s, lane) * hm_n, inc = warp_scan(w, lane);
-      int64_t start;
-      PlanRec r = part_of(a, __shfl_sync(0xffffffffu, inc, 31), &start);
+      const int nq = query_tiles(a, s);
+      int longest;
+      int64_t w = seq_steps(a, s, lane, 0, &longest);
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      // capped: 32 sequences of 2^30 tokens would not fit an int
+      const int units = __reduce_add_sync(0xffffffffu, nq < kMaxPagedCtas ? nq : kMaxPagedCtas);
+      int P = own_part(units, a.own_units, longest, a.own_steps, a.join_here ? kJoinHere : 0);
+      int64_t inc = 0, start = blockIdx.x;
+      PlanRec r = {};
+      const bool own = P && P + a.extra <= a.min_steps + a.slack;  // whatever the line's are
+      if (!own) {
+        w = (w + int64_t(nq) * a.extra) * hm_n;
+        inc = warp_scan(w, lane);
+        const int64_t total = __shfl_sync(0xffffffffu, inc, 31), per = line_part(a, total);
+        if (P + a.extra > per + a.slack) P = 0;
+        if (!P) r = part_of(a, total, per, &start);
+      }
+      if (P) {
+        w = hm_n * (P >= longest ? nq : int(seq_steps(a, s, lane, P, &longest)));
+        inc = warp_scan(int(w), lane);
+        r.count = start < __shfl_sync(0xffffffffu, inc, 31);
+      }
       if (r.count > 0) {
         const int src = __ffs(__ballot_sync(0xffffffffu, inc > start)) - 1;
         r.b = src;
         r.s = seq_of_lane(s, src);
-        find_in_seq(a, r, start - __shfl_sync(0xffffffffu, inc - w, src), lane);
+        find_in_seq(a, r, start - __shfl_sync(0xffffffffu, inc - w, src), P, lane);
       }
       if (lane == 0) {
         *rec = r;
@@ -213,7 +274,9 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
   for (int base = 0; base < a.B; base += kThreads) {
     const int b = base + tid;
     const Seq s = b < a.B ? load_seq(a, b) : none;
-    const int64_t inc = warp_scan(seq_lengths(a, s, lane) * hm_n, lane);
+    int longest;
+    const int64_t inc = warp_scan(
+        (seq_steps(a, s, lane, 0, &longest) + int64_t(query_tiles(a, s)) * a.extra) * hm_n, lane);
     if (lane == 31) warp_tot[warp] = inc;
     __syncthreads();
     int64_t before = carry, all = 0;
@@ -228,7 +291,7 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
   }
   if (warp == 0) {
     int64_t start;
-    PlanRec r = part_of(a, carry, &start);
+    PlanRec r = part_of(a, carry, line_part(a, carry), &start);
     if (r.count > 0) {
       int lo = 0, hi = a.B - 1;  // the sequence with cum[b] <= start < cum[b + 1]
       while (lo < hi) {
@@ -238,7 +301,7 @@ __device__ __forceinline__ void plan_part(const PagedArgs& a, int64_t* scratch, 
       }
       r.b = lo;
       r.s = load_seq(a, lo);
-      find_in_seq(a, r, start - cum[lo], lane);
+      find_in_seq(a, r, start - cum[lo], 0, lane);
     }
     if (lane == 0) {
       *rec = r;
@@ -267,13 +330,15 @@ struct Walk {
     if (left > 0) {
       s = r.s;
       t = tile_span(a, s, qt);
-      cut(a);
+      cut(r.extra);
       if (count == 0) next(a);
     }
   }
   __device__ __forceinline__ bool done() const { return left <= 0; }
   __device__ __forceinline__ bool whole() const { return first == 0 && count == t.n; }
   __device__ __forceinline__ int slot() const { return 2 * int(blockIdx.x) + (first > 0 ? 0 : 1); }
+  // (A part of a unit that is cut by itself is the CTA's only one: `left` is at most
+  // what is left of the unit.)
   __device__ __forceinline__ void next(const PagedArgs& a) {
     do {
       left -= t.n + a.extra - at;
@@ -290,20 +355,20 @@ struct Walk {
         }
         t = tile_span(a, s, qt);
       }
-      cut(a);
+      cut(a.extra);
     } while (count == 0);
   }
   // The first part boundary that cuts the unit's steps, and the CTAs that share
   // them.
-  __device__ __forceinline__ int cut_at(const PagedArgs& a, int per, int* parts) const {
-    const int c = int((from + a.extra) / per) + 1;
-    *parts = int((from + t.n + a.extra - 1) / per) - c + 2;
+  __device__ __forceinline__ int cut_at(int per, int extra, int* parts) const {
+    const int c = int((from + extra) / per) + 1;
+    *parts = int((from + t.n + extra - 1) / per) - c + 2;
     return c;
   }
-  __device__ __forceinline__ void cut(const PagedArgs& a) {
-    const int end = t.n + a.extra - at < left ? t.n + a.extra : at + left;
-    first = at > a.extra ? at - a.extra : 0;
-    count = end > a.extra ? end - a.extra - first : 0;
+  __device__ __forceinline__ void cut(int extra) {
+    const int end = t.n + extra - at < left ? t.n + extra : at + left;
+    first = at > extra ? at - extra : 0;
+    count = end > extra ? end - extra - first : 0;
   }
 };
 
@@ -323,13 +388,6 @@ __device__ __forceinline__ float tanh_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
   return fmaf(-2.f, r, 1.f);
 }
-
-// Most partials that the last CTA of a unit merges itself.  Measured (131 keys,
-// one sequence of 8 KV heads: no unit cut in two, but that is the GPU's to know): 8.6
-// us a call with the merge inside, 11.7 with a join kernel behind; with 37
-// partials a unit (200k keys) 140 us inside, 133 with the kernel, whose CTAs share
-// the rows.
-constexpr int kJoinHere = 8;
 
 // Whether no unit can be cut into more than kJoinHere parts.  A unit is at most as
 // long as the page table allows, a part at least min_steps; and the units of a

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   const PlanRec& r = a.rec[c];
   // boundary c cuts the steps of a unit, and the previous one does not
   const int count = r.count, j = r.j, per = r.per;
-  if (count == 0 || j <= a.extra || j - per > a.extra) return;
+  if (count == 0 || j <= r.extra || j - per > r.extra) return;
   constexpr int kVec = D / 32;
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];

@@ -52,6 +52,38 @@ FKV_HD Span tile_span(const TileRule& g, const Seq& s, int qt) {
 
 FKV_HD int block_at(const Span& t, int j) { return j < t.nA ? j : t.from + (j - t.nA); }
 
+// Division rounded down, 0 <= n < 2^22, k > 0: a quotient in floats is off by less
+// than one (half the code of an integer division, of which a short call runs more
+// than of anything else).
+constexpr int kDivMax = 1 << 22;
+FKV_HD int div_down(int n, int k) {
+#ifdef __CUDA_ARCH__
+  int q = int(__fdividef(float(n), float(k)));
+#else
+  int q = int(float(n) / float(k));
+#endif
+  const int r = n - q * k;
+  if (r < 0) --q;
+  if (r >= k) ++q;
+  return q;
+}
+// Parts of up to P steps of a unit of n steps (P = 0: its steps).
+FKV_HD int parts_of(int n, int P) { return P ? div_down(n + P - 1, P) : n; }
+
+// Length of the parts when every unit is cut by itself, into equal parts of at
+// least `least` steps and at most `most` parts (0: any), one per CTA; `slots` CTAs
+// per head for `units` units of at most `longest` steps.  0 when there are more
+// units than CTAs, or none, or a unit is out of div_down's range.
+FKV_HD int own_part(int units, int slots, int longest, int least, int most) {
+  if (units == 0 || units > slots || longest >= kDivMax / 2) return 0;
+  if (longest <= least) return longest;
+  int k = div_down(slots, units);
+  if (most && k > most) k = most;
+  const int p = parts_of(longest, k);
+  if (p <= least) return least;
+  return parts_of(longest, parts_of(longest, p));
+}
+
 // Keys of a row at position p besides the prefix: lo <= j <= hi.
 struct RowSpan {
   int lo, hi;

@@ -101,6 +101,12 @@ for _n, _dtype in ((33, "bf16"), (33, "fp32"), (400, "bf16")):
                                                q=[min((i * 37) % 90, (i * 5) % 7) for i in range(_n)], hk=1, g=2,
                                                D=64, page=8, dtype=_dtype, pad=2)
 ATTEND["window_beyond_all"] = Batch(kv=[3, 200], q=[9, 50], window=2 ** 31 - 1)
+# more units than CTAs of any of the kernels: cut on the line, most in two
+_LINE = [(i * 397) % 1100 for i in range(20)]
+for _dtype in ("bf16", "fp32"):
+    ATTEND[f"line_{_dtype}"] = Batch(kv=_LINE, q=[min(n, (i * 7) % 12) for i, n in enumerate(_LINE)], hk=24, g=1,
+                                     dtype=_dtype)
+    DECODE[f"line_{_dtype}"] = Batch(kv=_LINE, hk=24, g=1, dtype=_dtype)
 ATTEND["many_tiles"] = Batch(kv=[700, 600], q=[700, 600], hk=1, g=16)  # 88 and 75 query tiles
 
 

@@ -246,6 +246,24 @@ int main() {
     for (int o : owner)
       if (o != 1) return 8;
   }
+  // units cut by themselves: all parts fit the grid, none is empty, none but the
+  // last of a unit is shorter, and the division without integers is exact
+  for (int it = 0; it < 200000; ++it) {
+    const int units = rnd(200), slots = rnd(600), least = 1 + rnd(4), most = rnd(2) ? 0 : 1 + rnd(8);
+    const int longest = it & 1 ? 1 + rnd(40) : 1 + rnd(1 << 21);
+    const int P = own_part(units, slots, longest, least, most);
+    if ((units == 0 || units > slots) != (P == 0)) return 9;
+    if (P == 0) continue;
+    if (P > longest || (P < least && P != longest)) return 10;
+    const int k = parts_of(longest, P);
+    if (k != (longest + P - 1) / P || (k - 1) * P >= longest || int64_t(k) * P < longest) return 11;
+    if (int64_t(k) * units > slots || (most && k > most && P > least)) return 12;
+  }
+  if (own_part(1, 1, kDivMax / 2, 1, 0) != 0) return 13;
+  for (int it = 0; it < 1000000; ++it) {
+    const int k = 1 + (it & 1 ? rnd(700) : rnd(kDivMax)), n = it % 3 ? rnd(kDivMax) : rnd(kDivMax / k) * k;
+    if (div_down(n, k) != n / k) return 14;
+  }
   puts("ok");
   return 0;
 }

@@ -11,7 +11,7 @@
 // keeps the maxima, sums and outputs of its rows, so warps share nothing but the
 // key blocks.
 //
-// Measured: 1000 queries over 4000 keys, 16 heads, D = 128: 0.88 ms = 33 TFLOP/s
+// Measured: 1000 queries over 4000 keys, 16 heads, D = 128: 0.84 ms = 34 TFLOP/s
 // (14 with 16 rows per CTA and a lane per key, 29 with unpacked products).
 #include "paged_f32.cuh"
 

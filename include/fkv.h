@@ -500,7 +500,8 @@ int32_t fkv_step_fp8(const fkv_params_t* p, const fkv_step_io_t* io, const fkv_f
  * cu_q not ascending or above num_tokens (the sequence counts as empty),
  * kv_len outside 0 .. max_pages * page_size (clamped), a page id outside
  * 0 .. num_pages - 1 where a row is needed (an append drops the row; a read
- * sees rows of zeros), an appended token with a negative position (its key and
+ * sees rows of zeros; entries of pages that no query of the call sees may hold
+ * anything, so pages behind a window may be freed), an appended token with a negative position (its key and
  * value are dropped).  A query at a negative position is no error: under
  * FKV_PAGED_CAUSAL it sees the prefix alone. */
 #define FKV_PAGED_CAUSAL 1 /* query at position p sees keys j <= p; without it

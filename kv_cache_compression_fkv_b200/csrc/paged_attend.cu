@@ -123,7 +123,7 @@ __device__ __forceinline__ bool load_blocks(const PagedArgs& a, const Walk& w, c
     return block_at(w.t, w.first + st.step(hh, j)) * 128 + my_page * box_rows;
   };
   auto page_of = [&](int key) {
-    if (!boxed || key >= w.s.kv) return -1;
+    if (!boxed || !box_seen(w.s, w.t, key, box_rows)) return -1;
     const int id = page_id(a, w.b, key >> a.page_shift);
     return id < 0 ? (a.num_pages > 0 ? a.num_pages : 1) : id;  // bad: a page of zeros
   };

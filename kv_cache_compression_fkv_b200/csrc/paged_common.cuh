@@ -372,6 +372,14 @@ struct Walk {
   }
 };
 
+// Whether any row of a tile sees any of `rows` keys from `key` on.  Pages without
+// such a key may be gone (behind a window), and a copy of them is not worth its
+// bytes: their scores are masked and their values set to zero whatever the tile
+// holds.
+__device__ __forceinline__ bool box_seen(const Seq& s, const Span& t, int key, int rows) {
+  return key < s.pre || (key <= t.hi && key + rows > t.lo);
+}
+
 // Page id of a sequence's p-th page; -1 (reported) when out of range.
 __device__ __forceinline__ int page_id(const PagedArgs& a, int b, int p) {
   const int id = a.page_table[int64_t(b) * a.table_stride + p];

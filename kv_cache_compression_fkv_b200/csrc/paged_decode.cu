@@ -198,7 +198,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
       // this lane's page of step i (a bad id reads as zeros: a page past the end)
       auto page_of = [&](int i) {
         const int key = block_at(w.t, w.first + i) * kDecKeys + my_page * box_rows;
-        if (!boxed || key >= w.s.kv) return -1;
+        if (!boxed || !box_seen(w.s, w.t, key, box_rows)) return -1;
         const int id = page_id(a, w.b, key >> a.page_shift);
         return id < 0 ? (a.num_pages > 0 ? a.num_pages : 1) : id;
       };

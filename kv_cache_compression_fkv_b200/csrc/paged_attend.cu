@@ -80,29 +80,29 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-// x <- outer tanh(inner x) of 32 logits, tanh(y) = 1 - 2 / (e^2y + 1).  Four
-// denominators share one reciprocal, r = 1 / (d0 d1 d2 d3): the exponentials and
-// reciprocals are what a capped block waits for.  y is clamped to [-9, 9] (tanh is
-// within 3e-8 of 1 there), so the product stays below (e^18 + 1)^4 < 2e31.
+// x <- outer tanh(inner x) of 32 logits.  Four quotients share one reciprocal (the
+// denominators are at most 176 each).  2000 queries over 8000 keys, 16 heads: 269 us;
+// 259 with the tanh from an exponential, right to 2e-7 of the cap only.
 __device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float inner, float outer) {
-  const float k = inner * 2.885390081777927f, most = 9.f * 2.885390081777927f;  // 2 log2 e
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    float y[4], d[4];
+    float2 n[2], d[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[e] = __uint_as_float(x[i + e]) * k;
-      d[e] = ex2(fminf(fmaxf(y[e], -most), most)) + 1.f;  // finite, a NaN's too
-    }
-    const float p01 = d[0] * d[1], p23 = d[2] * d[3];
+    for (int e = 0; e < 2; ++e)
+      tanh_parts(mul2(make_float2(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])),
+                      make_float2(inner, inner)),
+                 n[e], d[e]);
+    const float p0 = d[0].x * d[0].y, p1 = d[1].x * d[1].y;
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(p01 * p23));
-    const float r01 = -2.f * r * p23, r23 = -2.f * r * p01;
-    const float t[4] = {fmaf(r01, d[1], 1.f), fmaf(r01, d[0], 1.f), fmaf(r23, d[3], 1.f),
-                        fmaf(r23, d[2], 1.f)};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)  // a NaN stays one, and with its own column
-      x[i + e] = __float_as_uint(y[e] != y[e] ? y[e] : outer * t[e]);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(p0 * p1));
+    r *= outer;
+    const float r0 = r * p1, r1 = r * p0;
+    const float2 t0 = mul2(n[0], mul2(make_float2(r0, r0), make_float2(d[0].y, d[0].x)));
+    const float2 t1 = mul2(n[1], mul2(make_float2(r1, r1), make_float2(d[1].y, d[1].x)));
+    x[i] = __float_as_uint(t0.x);
+    x[i + 1] = __float_as_uint(t0.y);
+    x[i + 2] = __float_as_uint(t1.x);
+    x[i + 3] = __float_as_uint(t1.y);
   }
 }
 

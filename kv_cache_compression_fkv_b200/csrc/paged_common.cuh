@@ -388,13 +388,51 @@ __device__ __forceinline__ int page_id(const PagedArgs& a, int b, int p) {
   return -1;
 }
 
-// c * tanh(x) without cancellation loss beyond one rounding of the absolute
-// value: tanh(x) = 1 - 2 / (e^2x + 1); exact limits at +-inf.
-__device__ __forceinline__ float tanh_fast(float x) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 2.885390081777927f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
-  return fmaf(-2.f, r, 1.f);
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// tanh(y) = num / den on pairs, num = y P(y^2), den = Q(y^2), |y| cut off at 8: within
+// 9 roundings relative to tanh(y), however small y is (coefficients from fit_tanh.py
+// beside this file).  (1 - 2 / (e^2y + 1) takes fewer instructions, but is within
+// 1e-7 of 1 and not of y: times a cap far above the scores that is all of them.)
+// A NaN comes out in its own num and leaves den finite.
+constexpr float kTanhMost = 8.f;
+__device__ __forceinline__ float cut_off(float y) {  // keeps a NaN
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(-kTanhMost));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(kTanhMost));
+  return y;
+}
+__device__ __forceinline__ void tanh_parts(float2 y, float2& num, float2& den) {
+  constexpr float P[5] = {9.999998212e-01f, 1.271007806e-01f, 2.694026800e-03f, 7.143671155e-06f,
+                          -6.107998107e-09f};
+  constexpr float Q[4] = {1.000000000e+00f, 4.604324698e-01f, 2.284044214e-02f, 1.964301337e-04f};
+  auto both = [](float c) { return make_float2(c, c); };
+  y.x = cut_off(y.x);
+  y.y = cut_off(y.y);
+  float2 u = mul2(y, y);
+  u.x = fminf(u.x, kTanhMost * kTanhMost);  // drops a NaN
+  u.y = fminf(u.y, kTanhMost * kTanhMost);
+  float2 p = fma2(both(P[4]), u, both(P[3]));
+#pragma unroll
+  for (int i = 2; i >= 0; --i) p = fma2(p, u, both(P[i]));
+  num = mul2(p, y);
+  den = fma2(both(Q[3]), u, both(Q[2]));
+#pragma unroll
+  for (int i = 1; i >= 0; --i) den = fma2(den, u, both(Q[i]));
 }
 
 // Whether no unit can be cut into more than kJoinHere parts.  A unit is at most as
@@ -427,23 +465,6 @@ inline PagedWs paged_ws_layout() {
 inline int paged_grid(int per_sm) {
   const int sms = num_sms();
   return per_sm * (sms < kMaxPagedSms ? sms : kMaxPagedSms);
-}
-
-// Two fp32 lanes per instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
-        "l"(*reinterpret_cast<uint64_t*>(&c)));
-  return *reinterpret_cast<float2*>(&r);
 }
 
 // Arguments of the norm / rotation / append kernel (paged_rows.cu).

@@ -286,7 +286,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = outer * tanh_fast(x[t][e] * inner);
+            for (int e = 0; e < 4; e += 2) {
+              float2 num, den;
+              float r;
+              tanh_parts(make_float2(x[t][e] * inner, x[t][e + 1] * inner), num, den);
+              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den.x * den.y));
+              r *= outer;
+              x[t][e] = num.x * (r * den.y);
+              x[t][e + 1] = num.y * (r * den.x);
+            }
         } else {
 #pragma unroll
           for (int t = 0; t < 2; ++t)

@@ -67,10 +67,12 @@ def attend_row(q, k, v, pos, *, scale, cap=0.0, slope=0.0, causal=True, window=0
     raw = k @ q * scale
     z = cap * np.tanh(raw / cap) if cap else raw
     dist = slope * (see - pos)
-    # fp32: the D products and sums of q.k, its scaling; the cap (within 4
-    # roundings of its absolute value c); the distance term and the sum; log2 e
+    # fp32: the D products and sums of q.k, its scaling; the cap, relative to the
+    # smaller of c and the score (the tanh within 9 roundings, the factors that
+    # enclose it and a shared reciprocal within 10; 3 in fp32); the distance term and
+    # the sum; log2 e
     dz = (D + 4) * U32 * np.max(np.abs(k) @ np.abs(q)) * scale
-    dz += 8 * U32 * (cap if cap else np.max(np.abs(raw)))
+    dz += 32 * U32 * min(cap, np.max(np.abs(raw))) if cap else 8 * U32 * np.max(np.abs(raw))
     dz += 4 * U32 * np.max(np.abs(dist)) + 4 * U32 * np.max(np.abs(z + dist))
     z = z + dist
     m = z.max()

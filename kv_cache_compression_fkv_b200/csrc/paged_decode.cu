@@ -187,7 +187,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
     bool ok = true;
     for (; ok && !w.done(); w.next(a), ++u) {
       const int h = w.hm / a.mt, m = w.hm - h * a.mt;
-      if (!(ok = mbar_wait(&bars->q_empty[u & 1], ((u >> 1) & 1) ^ 1, abort))) break;
+      if (!(ok = warp_wait(&bars->q_empty[u & 1], ((u >> 1) & 1) ^ 1, abort))) break;
       if (lane == 0) {
         mbar_expect_tx(&bars->q_full[u & 1], C::kQ);
         for (int half = 0; half < C::kHalves; ++half)
@@ -206,8 +206,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (int i = 0; i < steps; ++i, ++n) {
         const int next = i + 1 < steps ? page_of(i + 1) : 0;
         const uint32_t s = n % C::kStages, use = n / C::kStages;
-        ok = mbar_wait(&bars->empty[s], (use & 1) ^ 1, abort);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (!(ok = warp_wait(&bars->empty[s], (use & 1) ^ 1, abort))) break;
         const unsigned loads = __ballot_sync(0xffffffffu, id >= 0);
         if (lane == 0) {
           if (loads) mbar_expect_tx(&bars->full[s], __popc(loads) * uint32_t(box_rows) * 128);

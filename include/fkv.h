@@ -497,7 +497,8 @@ int32_t fkv_step_fp8(const fkv_params_t* p, const fkv_step_io_t* io, const fkv_f
  *
  * Device-side errors, recorded as FKV_ERR_DEVICE_ARG in the workspace status
  * word with the sequence as detail (nothing is read or written out of range):
- * cu_q not ascending or above num_tokens (the sequence counts as empty),
+ * cu_q not ascending or above num_tokens (the sequence counts as empty; rows that
+ * such offsets give to two sequences, or cut off behind cu_q[B], are unspecified),
  * kv_len outside 0 .. max_pages * page_size (clamped), a page id outside
  * 0 .. num_pages - 1 where a row is needed (an append drops the row; a read
  * sees rows of zeros; entries of pages that no query of the call sees may hold

@@ -72,33 +72,61 @@ struct Place {
   int live;          // 0: a padded row
 };
 
+// Reports bad offsets and lengths, of sequences without a token too: the warp of
+// token t looks after sequences t, t + tokens, ...
+__device__ __forceinline__ void check_seqs(const RowsArgs& a, int t, int lane) {
+  const int cap = a.max_pages << a.page_shift;
+  for (int64_t b = t + int64_t(lane) * a.tokens; b < a.B; b += int64_t(32) * a.tokens) {
+    const int kv = a.kv_len[b];
+    bool bad = kv < 0 || kv > cap;
+    if (a.cu_q) {
+      const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+      bad |= q0 < 0 || q1 < q0 || q1 > a.tokens;
+    }
+    if (bad) report(a.status, FKV_ERR_DEVICE_ARG, int(b));
+  }
+}
+
+// First sequence with good offsets around token t, by a scan; -1: none.  Only for
+// tokens whose search among bad offsets went astray.
+__device__ __noinline__ int scan_seq(const int32_t* cu_q, int B, int tokens, int t, int lane) {
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    const bool in = b < B && cu_q[b] >= 0 && cu_q[b] <= t && t < cu_q[b + 1] && cu_q[b + 1] <= tokens;
+    const unsigned found = __ballot_sync(0xffffffffu, in);
+    if (found) return b0 + __ffs(found) - 1;
+  }
+  return -1;
+}
+
 __device__ __forceinline__ Place find_place(const RowsArgs& a, int t, int lane) {
   Place p = {-1, 0, 0};
   int b = t, i = 0, q_len = 1;
   if (a.cu_q) {
     b = find_seq(a.cu_q, a.B, t, lane);
-    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.tokens) {
-      if (lane == 0) report(a.status, FKV_ERR_DEVICE_ARG, b);
-      return p;
+    int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+    if (t < q0 || t >= q1 || q0 < 0 || q1 > a.tokens) {
+      // behind the last offset (a padded row), or the offsets are not ascending
+      if (b == a.B - 1 && q0 >= 0 && q0 <= q1 && q1 <= t) return p;
+      b = scan_seq(a.cu_q, a.B, a.tokens, t, lane);
+      if (b < 0) return p;
+      q0 = a.cu_q[b];
+      q1 = a.cu_q[b + 1];
     }
     i = t - q0;
     q_len = q1 - q0;
-    if (i < 0 || i >= q_len) return p;
   }
   p.live = 1;
   const int cap = a.max_pages << a.page_shift;
   int kv = a.kv_len[b];
-  bool bad = kv < 0 || kv > cap;
-  if (bad) kv = kv < 0 ? 0 : cap;
+  kv = kv < 0 ? 0 : (kv > cap ? cap : kv);
   p.pos = kv - q_len + i;
   int id = -1;
   if (p.pos >= 0) id = a.page_table[int64_t(b) * a.table_stride + (p.pos >> a.page_shift)];
   if (id >= 0 && id < a.num_pages)
     p.page_off = int64_t(id) * a.page_stride + int64_t(p.pos & ((1 << a.page_shift) - 1)) * a.row_stride;
-  else
-    bad = true;
-  if (bad && lane == 0) report(a.status, FKV_ERR_DEVICE_ARG, b);
+  else if (lane == 0)
+    report(a.status, FKV_ERR_DEVICE_ARG, b);
   return p;
 }
 
@@ -182,6 +210,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a, int
   turn.adjacent = 0;
   Place place = {-1, 0, 1};
   if (a.append) {
+    if (blockIdx.y == 0) check_seqs(a, t, lane);
     place = find_place(a, t, lane);
     if (!place.live) return;
   }

@@ -549,7 +549,7 @@ static cudaError_t launch_attend(PagedArgs a, cudaStream_t s) {
   a.own_steps = 3;
   a.slack = 6;
   CUtensorMap tq, tk, tv;
-  if (!paged_tmaps(a, D, true, 128, a.mt == 1 ? a.G : 128, a.tq, &tq, &tk, &tv))
+  if (!paged_tmaps(a, D, 128, a.mt == 1 ? a.G : 128, a.tq, &tq, &tk, &tv))
     return cudaErrorNotSupported;
   const size_t smem = C::kOffBar + sizeof(PaBars);
   static_assert(C::kOffBar + sizeof(PaBars) <= 232448, "above the per-CTA limit");

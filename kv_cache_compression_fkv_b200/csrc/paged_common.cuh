@@ -496,10 +496,10 @@ struct RowsArgs {
 };
 
 cudaError_t launch_rows(const RowsArgs& a, bool bf16, int D, cudaStream_t s);
-// Tensor maps of a call's queries [tokens][Hq][D] (box: q_tokens x q_heads rows of
-// 128 bytes) and caches (box: the rows of a page, at most `keys`, of 128 bytes), all
-// in the 128-byte swizzle.  The x coordinate counts 16-bit words.
-bool paged_tmaps(const PagedArgs& a, int D, bool bf16, int keys, int q_heads, int q_tokens, CUtensorMap* q,
+// Tensor maps of a bf16 call's queries [tokens][Hq][D] (box: q_tokens x q_heads rows of
+// 64 dims) and caches (box: the rows of a page, at most `keys`, of 64 dims), all in the
+// 128-byte swizzle.
+bool paged_tmaps(const PagedArgs& a, int D, int keys, int q_heads, int q_tokens, CUtensorMap* q,
                  CUtensorMap* k, CUtensorMap* v);
 cudaError_t launch_paged_decode(const PagedArgs& a, int D, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedArgs& a, int D, cudaStream_t s);

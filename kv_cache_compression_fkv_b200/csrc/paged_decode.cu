@@ -500,7 +500,7 @@ static cudaError_t launch_decode(PagedArgs a, cudaStream_t s) {
   a.own_steps = 3;
   a.slack = 3;
   CUtensorMap tq, tk, tv;
-  if (!paged_tmaps(a, D, true, kDecKeys, kDecRows, 1, &tq, &tk, &tv)) return cudaErrorNotSupported;
+  if (!paged_tmaps(a, D, kDecKeys, kDecRows, 1, &tq, &tk, &tv)) return cudaErrorNotSupported;
   const size_t smem = 1024 + C::kOffBar + sizeof(DecBars);
   static_assert(C::kStages * C::kStage >= kPlanScratch, "the division's prefix sums fit in the ring");
   static_assert(2 * (1024 + C::kOffBar + sizeof(DecBars) + 1024 + 256) <= 233472,

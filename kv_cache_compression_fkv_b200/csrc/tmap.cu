@@ -60,9 +60,7 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t sl
   return r == CUDA_SUCCESS;
 }
 
-// Map of rows of 128-byte columns in the 128-byte swizzle.  Elements are 16-bit
-// words whatever the type (fp32 rows are twice as many): the copies only move
-// bytes.
+// Map of bf16 rows in columns of 64, in the 128-byte swizzle.
 static bool encode_rows(CUtensorMap* map, const void* base, uint32_t rank, const cuuint64_t* dims,
                         const cuuint64_t* strides, const cuuint32_t* box) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
@@ -73,23 +71,22 @@ static bool encode_rows(CUtensorMap* map, const void* base, uint32_t rank, const
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool paged_tmaps(const PagedArgs& a, int D, bool bf16, int keys, int q_heads, int q_tokens,
-                 CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
-  const cuuint64_t elem = bf16 ? 2 : 4;
-  const cuuint64_t row = cuuint64_t(D) * elem;  // bytes; also the stride of a dimension of one entry
-  const cuuint64_t q_dims[3] = {row / 2, cuuint64_t(a.Hq), cuuint64_t(a.num_tokens)};
-  const cuuint64_t q_strides[2] = {a.Hq > 1 ? cuuint64_t(a.q_hs) * elem : row,
-                                   a.num_tokens > 1 ? cuuint64_t(a.q_ts) * elem : row};
+bool paged_tmaps(const PagedArgs& a, int D, int keys, int q_heads, int q_tokens, CUtensorMap* q,
+                 CUtensorMap* k, CUtensorMap* v) {
+  const cuuint64_t row = cuuint64_t(D) * 2;  // bytes; also the stride of a dimension of one entry
+  const cuuint64_t q_dims[3] = {cuuint64_t(D), cuuint64_t(a.Hq), cuuint64_t(a.num_tokens)};
+  const cuuint64_t q_strides[2] = {a.Hq > 1 ? cuuint64_t(a.q_hs) * 2 : row,
+                                   a.num_tokens > 1 ? cuuint64_t(a.q_ts) * 2 : row};
   const cuuint32_t q_box[3] = {64, cuuint32_t(q_heads), cuuint32_t(q_tokens)};
   if (!encode_rows(q, a.q, 3, q_dims, q_strides, q_box)) return false;
   // A cache without pages gets a map of one page that no copy reads (every page
   // id is then out of range, and reads as the zeros outside the map).
   const bool none = a.num_pages == 0;
   const int rows = 1 << a.page_shift;
-  const cuuint64_t dims[4] = {row / 2, cuuint64_t(rows), cuuint64_t(a.Hkv),
+  const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(rows), cuuint64_t(a.Hkv),
                               cuuint64_t(none ? 1 : a.num_pages)};
-  const cuuint64_t strides[3] = {cuuint64_t(a.row_stride) * elem, cuuint64_t(a.head_stride) * elem,
-                                 cuuint64_t(a.page_stride) * elem};
+  const cuuint64_t strides[3] = {cuuint64_t(a.row_stride) * 2, cuuint64_t(a.head_stride) * 2,
+                                 cuuint64_t(a.page_stride) * 2};
   const cuuint32_t box[4] = {64, cuuint32_t(rows < keys ? rows : keys), 1, 1};
   return encode_rows(k, none ? a.q : a.k_cache, 4, dims, strides, box) &&
          encode_rows(v, none ? a.q : a.v_cache, 4, dims, strides, box);

@@ -24,13 +24,15 @@ CASES = {
 }
 
 
-def cut_boundaries(s, ctas):
-    """Part boundaries inside a unit's steps, from the records that the division
-    leaves in the workspace (paged_common.cuh, PlanRec: twelve ints, the fourth the
-    place inside the unit, the seventh the length of the part, the eighth what units
-    cost besides their steps)."""
+def division(s, ctas):
+    """Part boundaries inside a unit's steps, and whether units are cut by themselves,
+    from the records that the division leaves in the workspace (paged_common.cuh,
+    PlanRec: twelve ints, the fourth the place inside the unit, the seventh the length
+    of the part, the eighth what units cost besides their steps, 0 for cuts by
+    themselves)."""
     rec = s["ws"][256:256 + 48 * ctas].view(torch.int32).view(ctas, 12).cpu().numpy()
-    return int(np.sum((rec[:, 6] > 0) & (rec[:, 3] > rec[:, 7])))
+    rec = rec[rec[:, 6] > 0]
+    return int(np.sum(rec[:, 3] > rec[:, 7])), bool(np.all(rec[:, 7] == 0))
 
 
 @pytest.mark.parametrize("name", CASES)
@@ -45,7 +47,8 @@ def test_cut_units_are_joined(cuda_device, name):
     names = [e.name for e in prof.events()]
     assert sum("paged_decode_kernel" in n for n in names) == 1, names
     assert sum("paged_join_kernel" in n for n in names) == (0 if inside else 1), names
-    assert cut_boundaries(s, 2 * torch.cuda.get_device_properties(0).multi_processor_count) >= 2
+    cuts, own = division(s, 2 * torch.cuda.get_device_properties(0).multi_processor_count)
+    assert cuts >= 2 and (own or not name.startswith("own")) and (not own or not name.startswith("line"))
     check(case, s)
     assert status(s)[0] == 0
     first = s["out"].clone()

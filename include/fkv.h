@@ -55,10 +55,14 @@ extern "C" {
 
 /* 3: adds fkv_fp8_cache_t and the three *_fp8 entry points;
  * 4: adds fkv_select_heuristic; 5: adds fkv_step_fp8;
- * 6: adds fkv_diag_attend_timeout, fkv_diag_mma_rate, fkv_diag_ex2_rate, and
- *    (no earlier struct or entry point changed) the paged cache: fkv_paged_t
- *    and the fkv_paged_* entry points, fkv_qk_norm_rope. */
+ * 6: adds fkv_diag_attend_timeout, fkv_diag_mma_rate, fkv_diag_ex2_rate.
+ * Added without a new number, since nothing earlier changed: the paged cache
+ * (fkv_paged_t, the fkv_paged_* entry points, fkv_qk_norm_rope).  A caller that may
+ * meet an older library of version 6 looks for the symbol
+ * fkv_paged_workspace_size; one that compiles against an older header tests
+ * FKV_HAS_PAGED. */
 #define FKV_ABI_VERSION 6
+#define FKV_HAS_PAGED 1
 
 typedef enum fkv_status {
   FKV_OK = 0,
@@ -605,7 +609,11 @@ int32_t fkv_paged_decode(const fkv_paged_t* c, const fkv_rows_t* q, const fkv_ro
 /* The same for a ragged batch of num_tokens query tokens (cu_q; q, out:
  * [num_tokens][Hq][D], lse [num_tokens][Hq]).  Keys and values that no query
  * of the sequence sees may hold anything; keys and values that some query of
- * the sequence sees must be finite. */
+ * the sequence sees must be finite.  In bf16 each probability is rounded to bf16
+ * once before its product with the values, as in fkv_attend_compressed, and one
+ * exponential in eight is within 9e-5 (fkv_paged_decode and fp32 keep both to fp32);
+ * scores must stay within +-2^30 there (the largest may otherwise overflow against
+ * its own rounded maximum). */
 int32_t fkv_paged_attend(const fkv_paged_t* c, int32_t num_tokens, const fkv_rows_t* q,
                          const fkv_rows_t* out, float* lse, void* ws, void* stream);
 

@@ -179,7 +179,8 @@ class PagedCache:
     page_size, Hkv, D] is passed as its ``transpose(1, 2)``).  page_table: int32
     [sequences, max_pages].  softcap, window, alibi_slopes and causal as in
     fkv_paged_t; scale defaults to 1 / sqrt(D).  The page table may be changed
-    in place between calls."""
+    in place between calls; entries of pages that no query of a call sees (behind
+    a window, say) may hold anything."""
 
     def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, *,
                  num_q_heads: int, scale: Optional[float] = None, softcap: float = 0.0,
@@ -289,7 +290,8 @@ def paged_attend(cache: PagedCache, kv_len: torch.Tensor, cu_q: Optional[torch.T
     """Attention of a ragged batch of query tokens, q and out [tokens, Hq, D],
     over the cached keys (fkv_paged_attend); kv_len and cu_q as in
     :func:`paged_append`, prefix_len and lse (float32 [tokens, Hq]) as in
-    :func:`paged_decode`."""
+    :func:`paged_decode`.  In bfloat16 the probabilities are rounded to bfloat16
+    before their product with the values."""
     tokens, hq = q.shape[0], cache.num_q_heads
     _call("fkv_paged_attend", cache._index, stream, cache._struct(kv_len, cu_q, prefix_len), tokens,
           cache._rows(q, "q", tokens, hq), cache._rows(out, "out", tokens, hq), cache._lse(lse, tokens),

@@ -139,8 +139,8 @@ def make_rope(omega: Optional[torch.Tensor] = None, *, axis_pairs: Optional[Sequ
     n = 0 if omega is None else int(omega.numel())
     if axis_pairs is None:
         axis_pairs = (n,)
-    if sum(axis_pairs) != n:
-        raise ValueError(f"axis_pairs {tuple(axis_pairs)} do not add up to the {n} frequencies")
+    if sum(axis_pairs) != n or min(axis_pairs, default=0) < 0:
+        raise ValueError(f"axis_pairs {tuple(axis_pairs)} do not split the {n} frequencies")
     return Rope(omega, axis_pairs, style, norm, eps, q_weight, k_weight)
 
 
@@ -186,6 +186,9 @@ class PagedCache:
                  num_q_heads: int, scale: Optional[float] = None, softcap: float = 0.0,
                  window: int = 0, causal: bool = True,
                  alibi_slopes: Optional[torch.Tensor] = None):
+        for name, n, least in (("num_q_heads", num_q_heads, 1), ("window", window, 0)):
+            if not least <= n < 2 ** 31:  # a C int would keep the low 32 bits
+                raise ValueError(f"{name} must lie in {least} .. 2^31 - 1, got {n}")
         if k_cache.dim() != 4 or k_cache.dtype not in _DTYPES:
             raise ValueError("k_cache must be [num_pages, Hkv, page_size, D] in bfloat16 or float32")
         if (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or

@@ -242,8 +242,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         ldsm4(qf[k], q_addr + sw_off<kDecRows>(lane & 15, 2 * k + (lane >> 4)));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q_empty[u & 1]);
       float slope[2] = {0.f, 0.f};
       if (a.slopes) {
 #pragma unroll
@@ -378,6 +376,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
       }
       if (!ok) break;
+      // The queries are given back here and not behind their loads above: an arrive
+      // does not wait for fragments that are still on their way to registers, and the
+      // copy of the next unit but one, issued at once, then overtook them (runs of
+      // one-block units came out wrong now and then).  Behind the blocks all of them
+      // have been used; the next unit's queries lie in the other slot meanwhile.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_empty[u & 1]);
       // ---- merge the warps in the stage read last (still held)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {

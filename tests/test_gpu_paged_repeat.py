@@ -1,0 +1,38 @@
+"""Calls that repeat themselves bit for bit, on batches whose CTAs run through many
+short units: what one unit leaves in shared memory is not the next one's before it is
+done with."""
+import pytest
+import torch
+
+from tests.paged_util import Batch, attend, check, decode, status
+
+pytestmark = pytest.mark.gpu
+
+MIXED = [36, 118, 19, 4004, 50, 25, 7186, 17, 2500, 19, 64, 25, 36, 3000, 50, 1]
+CASES = {
+    "short_between_long": Batch(kv=(MIXED * 4)[:56], hk=8, g=4, nan=False),
+    "short_between_long_d64": Batch(kv=(MIXED * 4)[:56], hk=8, g=4, D=64, nan=False),
+    "all_short": Batch(kv=[1 + (i * 13) % 64 for i in range(700)], hk=8, g=2, nan=False),
+    "all_short_d64": Batch(kv=[1 + (i * 13) % 64 for i in range(700)], hk=8, g=2, D=64, nan=False),
+    "slices": Batch(kv=[1 + (i * 13) % 64 for i in range(200)], hk=4, g=40, nan=False),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("op", ["decode", "attend"])
+@pytest.mark.parametrize("name", CASES)
+def test_repeats(cuda_device, op, name, dtype):
+    case = Batch(**{**CASES[name].__dict__, "dtype": dtype})
+    s = case.make()
+    run = decode if op == "decode" else attend
+    run(s)
+    first, lse = s["out"].clone(), s["lse"].clone()
+    some = range(0, len(case.kv), max(1, len(case.kv) // 24))
+    check(case, s, only=set(some))
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(150):
+        s["out"].fill_(7.0)
+        run(s)
+        wrong += (s["out"] != first).any() | (s["lse"] != lse).any()
+    assert int(wrong) == 0
+    assert status(s)[0] == 0

@@ -89,28 +89,39 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 // x <- outer tanh(inner x) of 32 logits.  Four quotients share one reciprocal (the
-// denominators are at most 176 each).  2000 queries over 8000 keys, 16 heads: 269 us;
-// 259 with the tanh from an exponential, right to 2e-7 of the cap only.
+// denominators are at most 176 each).
 __device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float inner, float outer) {
+  float most = 0.f;  // a NaN is left out of it, and comes out of both forms as one
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                          make_float2(inner, inner));
+    most = fmax3(most, fabsf(y.x), fabsf(y.y));
+    x[i] = __float_as_uint(y.x);
+    x[i + 1] = __float_as_uint(y.y);
+  }
+  auto pair = [&](int i) { return make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])); };
+  auto put = [&](int i, float2 v) {
+    x[i] = __float_as_uint(v.x);
+    x[i + 1] = __float_as_uint(v.y);
+  };
+  if (!__any_sync(0xffffffffu, most >= kTanhSmall)) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) put(i, mul2(tanh_small(pair(i)), make_float2(outer, outer)));
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     float2 n[2], d[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      tanh_parts(mul2(make_float2(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])),
-                      make_float2(inner, inner)),
-                 n[e], d[e]);
+    for (int e = 0; e < 2; ++e) tanh_parts(pair(i + 2 * e), n[e], d[e]);
     const float p0 = d[0].x * d[0].y, p1 = d[1].x * d[1].y;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(p0 * p1));
     r *= outer;
     const float r0 = r * p1, r1 = r * p0;
-    const float2 t0 = mul2(n[0], mul2(make_float2(r0, r0), make_float2(d[0].y, d[0].x)));
-    const float2 t1 = mul2(n[1], mul2(make_float2(r1, r1), make_float2(d[1].y, d[1].x)));
-    x[i] = __float_as_uint(t0.x);
-    x[i + 1] = __float_as_uint(t0.y);
-    x[i + 2] = __float_as_uint(t1.x);
-    x[i + 3] = __float_as_uint(t1.y);
+    put(i, mul2(n[0], mul2(make_float2(r0, r0), make_float2(d[0].y, d[0].x))));
+    put(i + 2, mul2(n[1], mul2(make_float2(r1, r1), make_float2(d[1].y, d[1].x))));
   }
 }
 

@@ -410,7 +410,18 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // beside this file).  (1 - 2 / (e^2y + 1) takes fewer instructions, but is within
 // 1e-7 of 1 and not of y: times a cap far above the scores that is all of them.)
 // A NaN comes out in its own num and leaves den finite.
-constexpr float kTanhMost = 8.f;
+// Where all of a warp's |y| are below 1/2 (caps of 30 to 50 over ordinary scores)
+// tanh_small does with half the instructions: y + y^3 p(y^2), within 2 roundings.
+constexpr float kTanhMost = 8.f, kTanhSmall = 0.5f;
+__device__ __forceinline__ float2 tanh_small(float2 y) {
+  constexpr float S[4] = {-3.333314359e-01f, 1.332587898e-01f, -5.304549262e-02f, 1.724149100e-02f};
+  auto both = [](float c) { return make_float2(c, c); };
+  const float2 u = mul2(y, y);
+  float2 p = fma2(both(S[3]), u, both(S[2]));
+#pragma unroll
+  for (int i = 1; i >= 0; --i) p = fma2(p, u, both(S[i]));
+  return fma2(mul2(y, u), p, y);
+}
 __device__ __forceinline__ float cut_off(float y) {  // keeps a NaN
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(-kTanhMost));
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(kTanhMost));

@@ -280,17 +280,33 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
         const bool all = (k0 >= w.t.lo && k0 + 15 <= w.t.hi) || k0 + 15 < w.s.pre;
         if (a.cap > 0.f) {
           const float inner = a.scale / a.cap, outer = a.cap * kLog2e;
+          float most = 0.f;  // without the NaN, which come out of both forms as such
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[t][e] *= inner;
+              most = fmaxf(most, fabsf(x[t][e]));
+            }
+          const bool small = !__any_sync(0xffffffffu, most >= kTanhSmall);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              float2 num, den;
-              float r;
-              tanh_parts(make_float2(x[t][e] * inner, x[t][e + 1] * inner), num, den);
-              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den.x * den.y));
-              r *= outer;
-              x[t][e] = num.x * (r * den.y);
-              x[t][e + 1] = num.y * (r * den.x);
+              const float2 y = make_float2(x[t][e], x[t][e + 1]);
+              float2 v;
+              if (small) {
+                v = mul2(tanh_small(y), make_float2(outer, outer));
+              } else {
+                float2 num, den;
+                float r;
+                tanh_parts(y, num, den);
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den.x * den.y));
+                r *= outer;
+                v = make_float2(num.x * (r * den.y), num.y * (r * den.x));
+              }
+              x[t][e] = v.x;
+              x[t][e + 1] = v.y;
             }
         } else {
 #pragma unroll

@@ -31,11 +31,12 @@
 // rounding of its maximum: normalised away for scores up to 2^30, an overflow from
 // 2^31 on (the bound is the entry point's).
 //
-// Measured (back to back, under the power cap): the 480P chunk over 32760 keys, 942
-// GFLOP, 0.86 ms = 1099 TFLOP/s (0.67 of the burst GEMM, 0.79 of the sustained one);
-// two causal prompts, 637 GFLOP, 0.72 ms; 12 short pieces of capped and biased
-// scores 31 us, most of it one or two blocks' latency per CTA.  Per block and
-// stream the softmax takes 2.1k cycles and waits 2k for its next logits.
+// Measured (on the GPU, under the power cap; calls from Python in brackets): the 480P
+// chunk over 32760 keys, 942 GFLOP, 0.86 to 0.92 ms = 1020 to 1100 TFLOP/s (0.99 ms,
+// 951: 0.58 of the burst GEMM, 0.68 of the sustained one); two causal prompts, 637
+// GFLOP, 0.72 to 0.75 ms (0.79); 12 short pieces of capped and biased scores 28 us
+// (29), most of it one or two blocks' latency per CTA.  Per block and stream the
+// softmax takes 2.1k cycles and waits 2k for its next logits.
 #include "paged_sm100.cuh"
 
 namespace fkv {
@@ -89,7 +90,9 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 // x <- outer tanh(inner x) of 32 logits.  Four quotients share one reciprocal (the
-// denominators are at most 176 each).
+// denominators are at most 176 each).  2000 causal queries over 8000 keys, 16 heads:
+// 143 us without a cap, 222 with one of 50, where nearly all warps take the short
+// form, 276 with one of 5, where most take the quotient.
 __device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float inner, float outer) {
   float most = 0.f;  // a NaN is left out of it, and comes out of both forms as one
 #pragma unroll

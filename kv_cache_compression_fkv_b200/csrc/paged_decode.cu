@@ -18,10 +18,11 @@
 // error): the products are then as exact as fp32 weights, and the second MMA is
 // hidden behind the loads.
 //
-// Measured (8 KV heads, 32 query heads): 64 sequences of 17 .. 8191 keys, 725 MB,
-// 122 us = 0.91 of the copy bandwidth; one of 200001 keys, 819 MB, 133 us = 0.94;
-// one of 131 keys 8.7 us, of which the division of the work takes 1.8, the first
-// blocks 2.2 and the merge and store 1.2.
+// Measured (8 KV heads, 32 query heads; on the GPU, calls back to back in a graph;
+// calls from Python in brackets): 64 sequences of 17 .. 8191 keys, 725 MB, 122 us =
+// 0.91 of the copy bandwidth (130 = 0.85); one of 200001 keys, 819 MB, 135 us = 0.93
+// with its join (134); one of 131 keys 9.4 us (10.3), of which the division of the
+// work takes 1.8, the first blocks 2.2 and the merge and store 1.2.
 #include "paged_sm100.cuh"
 
 namespace fkv {
@@ -516,8 +517,9 @@ static cudaError_t launch_decode(PagedArgs a, cudaStream_t s) {
   a.min_steps = 4;
   a.extra = 1;
   // Units cut by themselves (own_steps 1 / 2 / 3): one sequence of 131 keys, 8 heads
-  // 11.2 / 11.8 / 10.1 us (on the line 9.9), of 1000 keys 14.2 / 12.0 / 13.2 (15.6);
-  // with slack 6 16 sequences of 100 to 1000 keys take 21.0 instead of 18.2.
+  // 10.3 / 10.7 / 9.3 us on the GPU (on the line 9.2), of 1000 keys 14.3 / 12.0 / 13.0
+  // (14.0), 16 sequences of 100 to 1000 keys 17.0 / 16.9 / 16.9 (16.7); with slack 6
+  // the last take a sixth longer.
   a.own_steps = 3;
   a.slack = 3;
   CUtensorMap tq, tk, tv;

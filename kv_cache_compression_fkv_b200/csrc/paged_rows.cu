@@ -11,9 +11,10 @@
 // formed and reduced to a fraction of a turn in fp64 (fp32 would lose 1e-2 radians
 // at position 10^5), the sine and cosine of the fraction in fp32.
 //
-// Measured: 14041 prompt tokens of 32 + 8 + 8 heads, 344 MB, 72 us = 0.73 of the
-// copy bandwidth (ncu: 25% of the warps resident, 2.1 instructions a cycle); a 480P
-// chunk, 57.5 MB, 15 us, of which the launch and the first loads take 5.  Slower or
+// Measured: 14002 prompt tokens of 32 + 8 + 8 heads, 344 MB, 69 us on the GPU = 0.76 of
+// the copy bandwidth, 71 a call (ncu: 23% of the warps resident, 2.1 instructions a
+// cycle); a 480P chunk, 57.5 MB, 15 us on the GPU with a cold L2, 16.5 a call, of which
+// the launch and the first loads take 5.  Slower or
 // equal: CTAs over four tokens with the cosines in shared memory (19 / 76 us; its
 // reads met in the banks), the rows staged by asynchronous copies (18 / 73), more
 // resident warps by fewer registers (21 / 82: spills).

@@ -409,7 +409,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
           const float m_new = fmaxf(m, bmax * sl2);
           if (j == 0) {
             m = m_new;
-          } else if (__any_sync(0xffffffffu, m_new > m + kPaRescale)) {
+          } else if (__any_sync(0xffffffffu, valid && m_new > m + kPaRescale)) {
+            // (rows that are not there hold anything and must not decide)
             // the PV before S_h(j) is complete, so O_h may be rescaled
             const float alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);
 #pragma unroll 1

@@ -36,3 +36,35 @@ def test_repeats(cuda_device, op, name, dtype):
         wrong += (s["out"] != first).any() | (s["lse"] != lse).any()
     assert int(wrong) == 0
     assert status(s)[0] == 0
+
+
+DIRT = {
+    "g5": Batch(kv=[900, 40, 333], q=[130, 3, 60], hk=2, g=5, nan=False),
+    "g3_d64": Batch(kv=[1500, 77], q=[300, 20], hk=2, g=3, D=64, nan=False),
+    "whole": Batch(kv=[1162, 300], q=[200, 33], hk=2, g=7, D=64, causal=False, nan=False),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("op", ["decode", "attend"])
+@pytest.mark.parametrize("name", DIRT)
+def test_results_do_not_go_by_what_was_there(cuda_device, op, name, dtype):
+    """Rows and keys that are not there hold what the last kernel left in shared
+    memory: here, calls over much larger or smaller numbers."""
+    case = Batch(**{**DIRT[name].__dict__, "dtype": dtype})
+    if op == "decode":
+        case = Batch(**{**case.__dict__, "kv": [n + i for n in case.kv for i in range(8)], "q": None,
+                        "prefix": [n for n in case.prefix for _ in range(8)] if case.prefix else None})
+    s = case.make()
+    run = decode if op == "decode" else attend
+    run(s)
+    check(case, s, only={0, 1})
+    first, lse = s["out"].clone(), s["lse"].clone()
+    for std in (100.0, 1e-3, 10.0):
+        dirt = Batch(kv=[640] * 40, q=None if op == "decode" else [256] * 40, hk=4, g=4, D=case.D, std=std, dtype=dtype,
+                     nan=False, page=128, causal=False).make()
+        for _ in range(3):
+            run(dirt)
+            s["out"].fill_(7.0)
+            run(s)
+            assert torch.equal(s["out"], first) and torch.equal(s["lse"], lse), std

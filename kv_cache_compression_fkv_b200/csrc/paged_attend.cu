@@ -91,15 +91,17 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 
 // x <- outer tanh(inner x) of 32 logits.  Four quotients share one reciprocal (the
 // denominators are at most 176 each).  2000 causal queries over 8000 keys, 16 heads:
-// 143 us without a cap, 222 with one of 50, where nearly all warps take the short
-// form, 276 with one of 5, where most take the quotient.
-__device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float inner, float outer) {
+// 143 us without a cap, 242 with one of 50, where nearly all warps take the short
+// form, 297 with one of 5, where most take the quotient.
+// `there`: the columns that the lane's row sees, one bit each (none, if the row is not
+// there); the others hold anything and must not decide which form the warp takes.
+__device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float inner, float outer, uint32_t there) {
   float most = 0.f;  // a NaN is left out of it, and comes out of both forms as one
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     const float2 y = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
                           make_float2(inner, inner));
-    most = fmax3(most, fabsf(y.x), fabsf(y.y));
+    most = fmax3(most, there >> i & 1u ? fabsf(y.x) : 0.f, there >> i & 2u ? fabsf(y.y) : 0.f);
     x[i] = __float_as_uint(y.x);
     x[i + 1] = __float_as_uint(y.y);
   }
@@ -373,16 +375,18 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tm_q,
               tmem_ld32(tS + c * 32, x);
               tmem_ld_wait();
               const int k = k0 + 32 * c;
-              if (a.cap > 0.f) cap_logits(x, a.scale / a.cap, a.cap / a.scale);
+              // columns that this row sees, one bit each
+              const uint32_t seen =
+                  full ? 0xffffffffu
+                       : low_bits(w.s.pre - k) | (low_bits(rs.hi + 1 - k) & ~low_bits(rs.lo - k));
+              if (a.cap > 0.f) cap_logits(x, a.scale / a.cap, a.cap / a.scale, valid ? seen : 0u);
               if (a.slopes) {
                 const float off = slope * float(k - pos);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   x[i] = __float_as_uint(__uint_as_float(x[i]) + fmaf(slope, float(i), off));
               }
-              if (!full) {  // columns that this row sees, one bit each
-                const uint32_t seen =
-                    low_bits(w.s.pre - k) | (low_bits(rs.hi + 1 - k) & ~low_bits(rs.lo - k));
+              if (!full) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (!(seen >> i & 1u)) x[i] = 0xff800000u;  // -inf

@@ -279,6 +279,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         // x[t][e]: key k0 + 8 t + col + (e & 1), head row quad + 8 (e >> 1)
         const bool all = (k0 >= w.t.lo && k0 + 15 <= w.t.hi) || k0 + 15 < w.s.pre;
+        uint32_t vmask[2] = {0xffffffffu, 0xffffffffu};  // keys that are seen, 16 bits each
+        if (!all) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            vmask[t] = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = k0 + 8 * t + col + e;
+              if (j < w.s.pre || (j >= w.t.lo && j <= w.t.hi)) vmask[t] |= 0xffffu << (16 * e);
+            }
+          }
+        }
+        auto seen = [&](int t, int e) { return (vmask[t] >> (16 * (e & 1)) & 1u) != 0; };
         if (a.cap > 0.f) {
           const float inner = a.scale / a.cap, outer = a.cap * kLog2e;
           float most = 0.f;  // without the NaN, which come out of both forms as such
@@ -286,7 +299,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              x[t][e] *= inner;
+              // (what is not seen may be anything and must not decide the form)
+              x[t][e] = all || seen(t, e) ? x[t][e] * inner : 0.f;
               most = fmaxf(most, fabsf(x[t][e]));
             }
           const bool small = !__any_sync(0xffffffffu, most >= kTanhSmall);
@@ -322,19 +336,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
             for (int e = 0; e < 4; ++e)
               x[t][e] = fmaf(slope[e >> 1], float(k0 + 8 * t + col + (e & 1) - p), x[t][e]);
         }
-        uint32_t vmask[2] = {0xffffffffu, 0xffffffffu};
         if (!all) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            vmask[t] = 0;
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = k0 + 8 * t + col + e;
-              const bool see = j < w.s.pre || (j >= w.t.lo && j <= w.t.hi);
-              if (see) vmask[t] |= 0xffffu << (16 * e);
-              else x[t][e] = x[t][e + 2] = -INFINITY;
-            }
-          }
+            for (int e = 0; e < 4; ++e)
+              if (!seen(t, e)) x[t][e] = -INFINITY;
         }
         float mn[2], ms[2];
 #pragma unroll

@@ -41,6 +41,10 @@ def test_repeats(cuda_device, op, name, dtype):
 DIRT = {
     "g5": Batch(kv=[900, 40, 333], q=[130, 3, 60], hk=2, g=5, nan=False),
     "g3_d64": Batch(kv=[1500, 77], q=[300, 20], hk=2, g=3, D=64, nan=False),
+    "cap": Batch(kv=[900, 40, 333], q=[130, 3, 60], hk=2, g=8, cap=30.0, std=1.5, nan=False),
+    "cap_g5_window": Batch(kv=[900, 40, 333], q=[130, 3, 60], hk=2, g=5, cap=30.0, std=1.5, window=50, prefix=[9, 0, 70],
+                           page=8, nan=False),
+    "cap_d64_slopes": Batch(kv=[700, 54], q=[90, 54], hk=1, g=7, D=64, cap=20.0, std=1.5, slopes=True, nan=False),
     "whole": Batch(kv=[1162, 300], q=[200, 33], hk=2, g=7, D=64, causal=False, nan=False),
 }
 

@@ -32,9 +32,9 @@
 // 2^31 on (the bound is the entry point's).
 //
 // Measured (on the GPU, under the power cap; calls from Python in brackets): the 480P
-// chunk over 32760 keys, 942 GFLOP, 0.86 to 0.92 ms = 1020 to 1100 TFLOP/s (0.99 ms,
-// 951: 0.58 of the burst GEMM, 0.68 of the sustained one); two causal prompts, 637
-// GFLOP, 0.72 to 0.75 ms (0.79); 12 short pieces of capped and biased scores 28 us
+// chunk over 32760 keys, 942 GFLOP, 0.85 to 0.89 ms = 1060 to 1115 TFLOP/s (0.98 ms,
+// 962: 0.58 of the burst GEMM, 0.69 of the sustained one); two causal prompts, 637
+// GFLOP, 0.70 to 0.80 ms (0.78); 12 short pieces of capped and biased scores 28 us
 // (29), most of it one or two blocks' latency per CTA.  Per block and stream the
 // softmax takes 2.1k cycles and waits 2k for its next logits.
 #include "paged_sm100.cuh"

@@ -20,7 +20,7 @@
 //
 // Measured (8 KV heads, 32 query heads; on the GPU, calls back to back in a graph;
 // calls from Python in brackets): 64 sequences of 17 .. 8191 keys, 725 MB, 122 us =
-// 0.91 of the copy bandwidth (130 = 0.85); one of 200001 keys, 819 MB, 135 us = 0.93
+// 0.91 of the copy bandwidth (124 to 131); one of 200001 keys, 819 MB, 135 us = 0.93
 // with its join (134); one of 131 keys 9.4 us (10.3), of which the division of the
 // work takes 1.8, the first blocks 2.2 and the merge and store 1.2.
 #include "paged_sm100.cuh"
